@@ -288,6 +288,78 @@ int fp4attn_dequant_bf16(const uint8_t* codes_dev, const uint8_t* scales_dev, co
 int fp4attn_dequant(const uint8_t* codes_dev, const uint8_t* scales_dev, const float* gscale_dev,
                     fp4attn_shape s, float* out_dev, cudaStream_t stream);
 
+/* ---- linear layers in NVFP4 ------------------------------------------------
+ * FastVideo "Pika H3 Flex in FastVideo", section "NVFP4 QAD": the linear layers
+ * around the attention take 4-bit weights and activations, one 8-bit scale per
+ * 16 values, under a per-tensor scale:
+ *   y[m][n] = g_x g_w sum_k x[m][k] w[n][k] + bias[n]
+ * with x and w the block-scaled E2M1 values of [M, K] activations and an
+ * [N, K] weight.
+ *   codes   uint8 [rows, K/2], element 2i in the low nibble of byte i
+ *   scales  uint8, fp4attn_scale_tile_bytes(rows, K) bytes: UE4M3 scales in
+ *           tiles of 128 rows x 64 channels, 512 bytes each, the tiles of one
+ *           128-row block in channel order: the scale of row r and block b
+ *           (channels 16b..16b+15) is byte
+ *             ((r/128) * ceil(K/64) + b/4) * 512 + (r%32)*16 + (r%128)/32*4 + b%4
+ *           (the order in which the tensor cores take them; scales of channels
+ *           past K are 0, those of rows past the last are never used)
+ * K is a multiple of 32 from 32 to 1048576; M and N are 0 to 4194304, odd ones
+ * included.  Pointers are 16-byte aligned, strides are in elements.
+ * The workspace of these calls holds a status word first (fp4attn_read_status,
+ * fp4attn_reset_status), which the caller clears once and the calls never
+ * clear; two calls that may overlap (other streams, two captured graphs
+ * replayed at once) need a workspace each. */
+
+/* Types of a row matrix. */
+enum { FP4ATTN_BF16 = 0, FP4ATTN_F32 = 1 };
+
+/* Bytes of the scale tiles of a [rows, K] matrix; 0 for a bad size. */
+size_t fp4attn_scale_tile_bytes(int64_t rows, int64_t K);
+
+/* Bytes of workspace of fp4attn_quantize_rows and fp4attn_gemm (any M, N, K)
+ * and of fp4attn_linear with these sizes.  Never 0. */
+size_t fp4attn_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* NVFP4 codes and scales of the rows of x: s = UE4M3(fl(fl(amax/6)/g)),
+ * code = E2M1(fl(x * fl(1/fl(g s)))) -- the steps of fp4attn_quantize_qk.
+ *   x_dev : [rows, K] bf16 or fp32 (x_type); x_stride, the elements from one
+ *     row to the next, a multiple of 8 (4 for fp32), at least K.
+ *   gscale_dev : device fp32 scalar g (finite, > 0), or NULL for 1; with
+ *     FP4ATTN_DYNAMIC_GSCALE in flags it is non-NULL and receives
+ *     g = fl32(amax of x / (6 * 448)), at least 2^-64.
+ *   codes_dev, scales_dev : out.
+ * Device errors: FP4ATTN_ERR_RANGE for a non-finite value or a bad g. */
+int fp4attn_quantize_rows(const void* x_dev, int x_type, int64_t x_stride, int64_t rows, int64_t K,
+                          float* gscale_dev, uint32_t flags, uint8_t* codes_dev, uint8_t* scales_dev,
+                          void* workspace_dev, size_t workspace_bytes, cudaStream_t stream);
+
+/* The values of quantised rows, fl(fl(g * s) * e2m1), contiguous [rows, K] in
+ * out_type (rounded to bf16; exact there for g a power of two). */
+int fp4attn_dequant_rows(const uint8_t* codes_dev, const uint8_t* scales_dev, const float* gscale_dev, int64_t rows,
+                         int64_t K, void* out_dev, int out_type, cudaStream_t stream);
+
+/* y = g_x g_w x w^T + bias of quantised x [M, K] and w [N, K].
+ *   bias_bf16_dev : [N] or NULL.  y_bf16_dev : [M, N] out, y_stride >= N
+ *   elements from one row to the next (any value; rows that start on 16 bytes
+ *   are stored fastest).
+ * The products of a row accumulate in fp32 in an order that depends on the
+ * sizes only: equal calls give equal bits.
+ * Device errors: FP4ATTN_ERR_RANGE for a bad g; FP4ATTN_ERR_TIMEOUT if an
+ * internal wait ran out. */
+int fp4attn_gemm(const uint8_t* x_codes_dev, const uint8_t* x_scales_dev, const float* x_gscale_dev,
+                 const uint8_t* w_codes_dev, const uint8_t* w_scales_dev, const float* w_gscale_dev,
+                 const void* bias_bf16_dev, int64_t M, int64_t N, int64_t K, void* y_bf16_dev, int64_t y_stride,
+                 void* workspace_dev, size_t workspace_bytes, cudaStream_t stream);
+
+/* fp4attn_gemm of bf16 x [M, K] (x_stride as for fp4attn_quantize_rows), which
+ * is quantised into the workspace on the way.
+ *   x_gscale_dev : as gscale_dev of fp4attn_quantize_rows; with
+ *     FP4ATTN_DYNAMIC_GSCALE it may be NULL (g then stays in the workspace). */
+int fp4attn_linear(const void* x_bf16_dev, int64_t x_stride, float* x_gscale_dev, uint32_t flags,
+                   const uint8_t* w_codes_dev, const uint8_t* w_scales_dev, const float* w_gscale_dev,
+                   const void* bias_bf16_dev, int64_t M, int64_t N, int64_t K, void* y_bf16_dev, int64_t y_stride,
+                   void* workspace_dev, size_t workspace_bytes, cudaStream_t stream);
+
 /* Read (synchronously: waits for the stream) and return in *device_status the
  * workspace status word: FP4ATTN_OK or the first device error. */
 int fp4attn_read_status(const void* workspace_dev, cudaStream_t stream, int* device_status);

@@ -1,0 +1,520 @@
+// The NVFP4 product of the linear layers: out[m][n] = g_x g_w sum_k x[m][k] w[n][k] + bias[n].
+//
+// FastVideo "Pika H3 Flex in FastVideo", section "NVFP4 QAD": every attention
+// and feed-forward linear takes 4-bit weights and activations with an 8-bit
+// scale per 16 values.  One persistent kernel on the block-scaled FP4 tensor
+// cores:
+//   * a tile is 128 rows of one operand (the lanes of TMEM) by TN rows of the
+//     other (its columns).  The lane side is x for long inputs; for short ones
+//     and for outputs whose rows do not start on 16 bytes it is w (`SWAP`):
+//     128 weight rows by the few rows of x, and a warp then stores 32
+//     consecutive outputs;
+//   * K goes by in stages of 256 values (128 code bytes: 128B-swizzled K-major
+//     tiles by TMA, and whole scale tiles by bulk copies) through a ring;
+//   * per stage the MMA warp copies the scale tiles to TMEM and issues one
+//     M=128, N=TN, K=64 tcgen05.mma for each 64 values;
+//   * two accumulators alternate, so the epilogue of one tile runs under the
+//     products of the next.  With TN = 256 both do not fit beside the scales:
+//     they overlap by OVERLAP columns, which the epilogue reads first and then
+//     releases;
+//   * SPLIT: few tiles and a long K.  A cluster shares one tile, each CTA a
+//     part of K; the fp32 parts are added in rank order through distributed
+//     shared memory, so the result does not depend on timing.
+// Every wait is bounded; a wait that runs out raises FP4ATTN_ERR_TIMEOUT in the
+// status word and the CTA winds down.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+
+#include "fp4_operands.cuh"
+#include "nvfp4_rows.cuh"
+
+namespace fp4attn {
+
+namespace {
+
+constexpr int BP = 128;       // rows of the lane-side operand per tile
+constexpr int BK = 256;       // K per stage
+constexpr int CHUNKS = BK / 64;
+constexpr int THREADS = 192;  // warps 0-3 epilogue, 4 producer, 5 MMA
+constexpr int WARP_PRODUCER = 4, WARP_MMA = 5;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t SF_COL = 448;  // scale factors: per 64-chunk 4 columns of the lane side, 4 or 8 of the other
+constexpr uint64_t kLimitNs = 2000000000ull;   // 2 s: far beyond any legitimate wait
+constexpr uint64_t kDrainNs = 200000000ull;    // 0.2 s for the wind-down waits
+
+__host__ __device__ constexpr int round128(int n) { return (n + 127) / 128 * 128; }
+
+template <int TN>
+struct Cfg {
+    static constexpr uint32_t P_BYTES = BP * BK / 2;
+    static constexpr uint32_t Q_BYTES = (uint32_t)(TN * BK / 2 + 1023) / 1024 * 1024;
+    static constexpr uint32_t SFP_BYTES = CHUNKS * 512;
+    static constexpr uint32_t SFQ_BYTES = (uint32_t)(round128(TN) / 128) * CHUNKS * 512;
+    static constexpr uint32_t STAGE = P_BYTES + Q_BYTES + SFP_BYTES + SFQ_BYTES;
+    static constexpr int STAGES = (int)((222u * 1024) / STAGE) < 8 ? (int)((222u * 1024) / STAGE) : 8;
+    static constexpr uint32_t ACC1 = TN == 256 ? 192 : TN;  // first column of the second accumulator
+    static constexpr int OVERLAP = TN == 256 ? 64 : 0;
+    static constexpr int SFQ_COLS = round128(TN) / 32;
+    static_assert(ACC1 + TN <= SF_COL, "TMEM: accumulators end before the scale factors");
+    static_assert(SF_COL + CHUNKS * (4 + SFQ_COLS) <= TMEM_COLS, "TMEM: scale factors");
+    static_assert(STAGE % 1024 == 0, "stages keep the swizzle's alignment");
+};
+
+struct Bars {
+    uint64_t full[8], empty[8];
+    uint64_t acc_full[2];
+    uint64_t next_ok;
+    uint64_t final_;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+struct GemmParams {
+    int P, Q;              // rows of the lane-side and of the column-side operand
+    int p_tiles, q_tiles;
+    int stages;            // K in stages of 256
+    int chunks;            // K in chunks of 64
+    const uint8_t* sfp;
+    const uint8_t* sfq;
+    int sfp_blocks, sfq_blocks;  // 128-row blocks of the two scale arrays
+    const float* gx;
+    const float* gw;
+    const __nv_bfloat16* bias;
+    __nv_bfloat16* out;
+    long long ld;
+    int N;
+    int x_is_p;            // x is the lane side (its copies wait for the quantiser)
+    int pdl;
+    int* status;
+};
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status, kLimitNs));
+}
+__device__ __forceinline__ bool drain_wait(uint32_t bar, uint32_t parity) {
+    int dummy = 0;
+    return mbar_wait(bar, parity, &dummy, nullptr, kDrainNs);
+}
+
+// Tiles in groups of 8 lane-side tiles, the group's column tiles outermost: a
+// wave of 148 tiles then reads about 8 + 18 operand tiles, not 148 of one side.
+constexpr int GROUP = 8;
+__device__ __forceinline__ void tile_of(int t, int p_tiles, int q_tiles, int& pt, int& qt) {
+    const int per = GROUP * q_tiles;
+    const int grp = t / per, in = t - grp * per;
+    const int rows = min(GROUP, p_tiles - grp * GROUP);
+    qt = in / rows;
+    pt = grp * GROUP + (in - qt * rows);
+}
+
+__device__ __forceinline__ uint64_t rows_desc(uint32_t addr) { return smem_desc(addr, 16, 1024, LAYOUT_SW128); }
+
+template <int TN, bool SWAP, bool SPLIT>
+__global__ void __launch_bounds__(THREADS, 1)
+    gemm_fp4_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
+                    const GemmParams p) {
+    using C = Cfg<TN>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Bars sm;
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t ring_u = smem_u32(ring);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n_tiles = p.p_tiles * p.q_tiles;
+    // SPLIT: the CTAs of a cluster share tile blockIdx.x / S
+    uint32_t rank = 0, ranks = 1;
+    if constexpr (SPLIT) {
+        asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+        asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+    }
+    const int first = SPLIT ? (int)(blockIdx.x / ranks) : (int)blockIdx.x;
+    const int step = SPLIT ? n_tiles : (int)gridDim.x;
+    const int s_begin = SPLIT ? (int)((long long)p.stages * rank / ranks) : 0;
+    const int s_end = SPLIT ? (int)((long long)p.stages * (rank + 1) / ranks) : p.stages;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(smem_u32(&sm.full[s]), 1);
+            mbar_init(smem_u32(&sm.empty[s]), 1);
+        }
+        mbar_init(smem_u32(&sm.acc_full[0]), 1);
+        mbar_init(smem_u32(&sm.acc_full[1]), 1);
+        mbar_init(smem_u32(&sm.next_ok), 4);
+        mbar_init(smem_u32(&sm.final_), 1);
+        sm.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == WARP_MMA) {
+        tmem_alloc(smem_u32(&sm.tmem_base), TMEM_COLS);
+        tmem_relinquish();
+    }
+    if (warp == WARP_PRODUCER && lane == 0) {
+        prefetch_tmap(&tm_p);
+        prefetch_tmap(&tm_q);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    volatile int* abort_flag = &sm.abort_flag;
+
+    if (warp == WARP_PRODUCER) {
+        // ------------------------------------------------------ producer --
+        // One operand is x, which the launch before may still be writing: the
+        // first stages of the weight go out before that launch is waited for.
+        int it = 0;
+        bool waited = p.pdl == 0;
+        auto copy_p = [&](int slot, int ks, int pt) {
+            const uint32_t full = smem_u32(&sm.full[slot]);
+            const uint32_t at = ring_u + C::STAGE * slot;
+            const int n = min(CHUNKS, p.chunks - CHUNKS * ks);
+            tma_load_2d(at, &tm_p, 128 * ks, BP * pt, full);
+            bulk_load(at + C::P_BYTES + C::Q_BYTES, p.sfp + ((long long)pt * p.chunks + CHUNKS * ks) * 512, 512u * n,
+                      full);
+        };
+        auto copy_q = [&](int slot, int ks, int qt) {
+            const uint32_t full = smem_u32(&sm.full[slot]);
+            const uint32_t at = ring_u + C::STAGE * slot;
+            const int n = min(CHUNKS, p.chunks - CHUNKS * ks);
+            tma_load_2d(at + C::P_BYTES, &tm_q, 128 * ks, TN * qt, full);
+#pragma unroll
+            for (int b = 0; b < round128(TN) / 128; ++b) {
+                const int rb = qt * (round128(TN) / 128) + b;
+                if (rb < p.sfq_blocks)
+                    bulk_load(at + C::P_BYTES + C::Q_BYTES + C::SFP_BYTES + CHUNKS * 512 * b,
+                              p.sfq + ((long long)rb * p.chunks + CHUNKS * ks) * 512, 512u * n, full);
+            }
+        };
+        auto bytes_of = [&](int ks, int qt) {
+            const int n = min(CHUNKS, p.chunks - CHUNKS * ks);
+            const int blocks = min(round128(TN) / 128, p.sfq_blocks - qt * (round128(TN) / 128));
+            return C::P_BYTES + (uint32_t)(TN * BK / 2) + 512u * n * (1 + blocks);
+        };
+        bool ok = true;
+        for (int t = first; ok && t < n_tiles; t += step) {
+            int pt, qt;
+            tile_of(t, p.p_tiles, p.q_tiles, pt, qt);
+            int ks = s_begin;
+            if (!waited) {
+                // the ring is empty: fill it with weight copies, wait, then x's
+                const int pre = min(C::STAGES, s_end - s_begin);
+                if (lane == 0) {
+                    for (int i = 0; i < pre; ++i) {
+                        mbar_arrive_expect_tx(smem_u32(&sm.full[i]), bytes_of(ks + i, qt));
+                        if (p.x_is_p) copy_q(i, ks + i, qt); else copy_p(i, ks + i, pt);
+                    }
+                }
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                if (lane == 0) {
+                    for (int i = 0; i < pre; ++i) {
+                        if (p.x_is_p) copy_p(i, ks + i, pt); else copy_q(i, ks + i, qt);
+                    }
+                }
+                __syncwarp();
+                waited = true;
+                it = pre;
+                ks += pre;
+            }
+            for (; ks < s_end; ++ks, ++it) {
+                const int slot = it % C::STAGES;
+                if (it >= C::STAGES &&
+                    !warp_wait(smem_u32(&sm.empty[slot]), (it / C::STAGES - 1) & 1, abort_flag, p.status)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(smem_u32(&sm.full[slot]), bytes_of(ks, qt));
+                    copy_p(slot, ks, pt);
+                    copy_q(slot, ks, qt);
+                }
+                __syncwarp();
+            }
+        }
+        if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (lane == 0 && *abort_flag) {
+            // wind down: this CTA's own copies land before it exits
+            for (int i = (it > C::STAGES ? it - C::STAGES : 0); i < it; ++i)
+                drain_wait(smem_u32(&sm.full[i % C::STAGES]), (i / C::STAGES) & 1);
+        }
+    } else if (warp == WARP_MMA) {
+        // ----------------------------------------------------------- MMA --
+        const bool leader = elect_one_sync();
+        constexpr uint32_t IDESC = idesc_mxf4(BP, TN);
+        auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+            return __all_sync(0xffffffffu, mbar_wait_spin(bar, parity, abort_flag, p.status, kLimitNs));
+        };
+        int it = 0, local = 0;
+        bool ok = true;
+        for (int t = first; ok && t < n_tiles; t += step, ++local) {
+            const uint32_t acc = tmem + (local & 1 ? C::ACC1 : 0u);
+            // the tile before has left the columns this one starts on (and
+            // with it every earlier tile all of its own)
+            if (local > 0 && !wait(smem_u32(&sm.next_ok), (local - 1) & 1)) break;
+            tc_fence_after();
+            for (int ks = s_begin; ks < s_end; ++ks, ++it) {
+                const int slot = it % C::STAGES;
+                if (!wait(smem_u32(&sm.full[slot]), (it / C::STAGES) & 1)) {
+                    ok = false;
+                    break;
+                }
+                if (leader) {
+                    tc_fence_after();
+                    const uint32_t at = ring_u + C::STAGE * slot;
+                    const uint32_t sf = at + C::P_BYTES + C::Q_BYTES;
+                    const int n = min(CHUNKS, p.chunks - CHUNKS * ks);
+                    const uint64_t pd = rows_desc(at), qd = rows_desc(at + C::P_BYTES);
+#pragma unroll
+                    for (int c = 0; c < CHUNKS; ++c) {
+                        if (c < n) {
+                            // one thread's copies and products run in the order issued
+                            const uint32_t ta = tmem + SF_COL + 4u * c;
+                            const uint32_t tb = tmem + SF_COL + 4u * CHUNKS + (uint32_t)C::SFQ_COLS * c;
+                            tmem_cp_32x128b_x4(ta, smem_desc(sf + 512 * c, 0, 128, LAYOUT_NONE));
+#pragma unroll
+                            for (int b = 0; b < round128(TN) / 128; ++b)
+                                tmem_cp_32x128b_x4(tb + 4u * b, smem_desc(sf + C::SFP_BYTES + CHUNKS * 512 * b + 512 * c,
+                                                                          0, 128, LAYOUT_NONE));
+                            mma_mxf4nvf4(acc, pd + 2u * c, qd + 2u * c, IDESC, ta, tb, (ks > s_begin || c > 0) ? 1u : 0u);
+                        }
+                    }
+                    tc_commit(smem_u32(&sm.empty[slot]));
+                    if (ks == s_end - 1) tc_commit(smem_u32(&sm.acc_full[local & 1]));
+                }
+                __syncwarp();
+            }
+        }
+        // every product this warp issued must finish before TMEM is freed
+        if (leader) {
+            tc_commit(smem_u32(&sm.final_));
+            drain_wait(smem_u32(&sm.final_), 0);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------ epilogue --
+        if (p.pdl) asm volatile("griddepcontrol.wait;" ::: "memory");
+        const float gx = p.gx ? __ldcg(p.gx) : 1.0f, gw = p.gw ? __ldg(p.gw) : 1.0f;
+        if (blockIdx.x == 0 && threadIdx.x == 0 && (bad_gscale(gx) || bad_gscale(gw)))
+            raise_status(p.status, FP4ATTN_ERR_RANGE);
+        const float g = __fmul_rn(gx, gw);
+        const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+        const int row = 32 * warp + lane;
+        int local = 0;
+        for (int t = first; t < n_tiles; t += step, ++local) {
+            int pt, qt;
+            tile_of(t, p.p_tiles, p.q_tiles, pt, qt);
+            const uint32_t acc = tmem + lanes + (local & 1 ? C::ACC1 : 0u);
+            if (!warp_wait(smem_u32(&sm.acc_full[local & 1]), (local >> 1) & 1, abort_flag, p.status)) break;
+            tc_fence_after();
+            const int pr = BP * pt + row;  // this thread's row of the lane side
+            const int q0 = TN * qt;
+            if constexpr (SPLIT) {
+                // the ring is idle now (every product of this CTA is done): the
+                // part goes there column by column, 128 rows each
+                float* part = reinterpret_cast<float*>(ring);
+#pragma unroll 1
+                for (int c0 = 0; c0 < TN; c0 += 16) {
+                    uint32_t r[16];
+                    tmem_ld16(acc + c0, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) part[(c0 + i) * BP + row] = __uint_as_float(r[i]);
+                }
+            } else {
+                constexpr int W = TN < 32 ? 16 : 32;  // columns per step
+                if constexpr (C::OVERLAP == 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sm.next_ok));
+                }
+                const float own_bias =
+                    (SWAP && p.bias && pr < p.P) ? __bfloat162float(p.bias[pr]) : 0.0f;
+                // the columns shared with the other accumulator first
+                constexpr int STEPS = TN / W, SHARED = C::OVERLAP / W;
+                const int start = (C::OVERLAP && !(local & 1)) ? STEPS - SHARED : 0;
+#pragma unroll 1
+                for (int i = 0; i < STEPS; ++i) {
+                    int c0 = start + i;
+                    c0 = (c0 >= STEPS ? c0 - STEPS : c0) * W;
+                    uint32_t r[W];
+                    if constexpr (W == 16) tmem_ld16(acc + c0, r); else tmem_ld32(acc + c0, r);
+                    tmem_wait_ld();
+                    if constexpr (C::OVERLAP != 0) {
+                        if (i == SHARED - 1) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(smem_u32(&sm.next_ok));
+                        }
+                    }
+                    if constexpr (SWAP) {
+                        // lane = column n of the output, c0 + k = its row m
+                        if (pr < p.P) {
+#pragma unroll
+                            for (int k = 0; k < W; ++k) {
+                                const int m = q0 + c0 + k;
+                                if (m < p.Q && FP4ATTN_IN_BOUNDS((long long)m * p.ld + pr <= (long long)(p.Q - 1) * p.ld + p.N - 1, p.status))
+                                    p.out[(long long)m * p.ld + pr] =
+                                        __float2bfloat16_rn(__fmaf_rn(__uint_as_float(r[k]), g, own_bias));
+                            }
+                        }
+                    } else {
+                        const int n0 = q0 + c0;
+                        float b = 0.0f;
+                        if (p.bias && n0 + lane < p.Q) b = __bfloat162float(p.bias[n0 + lane]);
+                        float v[W];
+#pragma unroll
+                        for (int k = 0; k < W; ++k)
+                            v[k] = __fmaf_rn(__uint_as_float(r[k]), g, __shfl_sync(0xffffffffu, b, k));
+                        if (pr < p.P && n0 < p.Q &&
+                            FP4ATTN_IN_BOUNDS((long long)pr * p.ld + n0 <= (long long)(p.P - 1) * p.ld + p.N - 1, p.status)) {
+                            __nv_bfloat16* dst = p.out + (long long)pr * p.ld + n0;
+#pragma unroll
+                            for (int j = 0; j < W / 8; ++j) {
+                                if (n0 + 8 * j < p.Q)  // Q is a multiple of 8 here
+                                    reinterpret_cast<uint4*>(dst)[j] =
+                                        make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                                                   pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+                            }
+                        }
+                    }
+                }
+            }
+        }
+        if constexpr (SPLIT) tc_fence_before();
+    }
+
+    if constexpr (SPLIT) {
+        // Every CTA's part is in its shared memory; rank r adds columns
+        // [r TN / ranks, (r + 1) TN / ranks) over the ranks in order.
+        namespace cg = cooperative_groups;
+        cg::cluster_group cl = cg::this_cluster();
+        __syncwarp();
+        cl.sync();
+        if (warp < 4) {
+            const float gx = p.gx ? __ldcg(p.gx) : 1.0f, gw = p.gw ? __ldg(p.gw) : 1.0f;
+            const float g = __fmul_rn(gx, gw);
+            int pt, qt;
+            tile_of(first, p.p_tiles, p.q_tiles, pt, qt);
+            const int row = threadIdx.x;  // 0..127
+            const int pr = BP * pt + row;
+            const float bias = (p.bias && pr < p.P) ? __bfloat162float(p.bias[pr]) : 0.0f;
+            float* part = reinterpret_cast<float*>(ring);
+            const int c_end = (int)(TN * (rank + 1) / ranks);
+            for (int c = (int)(TN * rank / ranks); c < c_end; ++c) {
+                const int m = TN * qt + c;
+                if (m >= p.Q) break;
+                float s = 0.0f;
+                for (uint32_t k = 0; k < ranks; ++k) s += cl.map_shared_rank(part, k)[c * BP + row];
+                if (pr < p.P && FP4ATTN_IN_BOUNDS((long long)m * p.ld + pr <= (long long)(p.Q - 1) * p.ld + p.N - 1, p.status))
+                    p.out[(long long)m * p.ld + pr] = __float2bfloat16_rn(__fmaf_rn(s, g, bias));
+            }
+        }
+        __syncwarp();
+        cl.sync();  // no CTA leaves while another reads its part
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == WARP_MMA) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+// Codes [rows][K/2 bytes]: 128B-swizzled boxes of 128 bytes x box_rows; rows
+// and bytes past the end read as zero codes.
+bool make_rows_code_map(CUtensorMap* m, const uint8_t* base, int64_t rows, int64_t K, uint32_t box_rows) {
+    const uint64_t dims[2] = {(uint64_t)K / 2, (uint64_t)rows};
+    const uint64_t strides[1] = {(uint64_t)K / 2};
+    const uint32_t box[2] = {128, box_rows};
+    return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box,
+                             CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int TN, bool SWAP, bool SPLIT>
+int launch_one(const GemmFp4Args& a, GemmParams& p, int split, int sms, cudaStream_t stream) {
+    using C = Cfg<TN>;
+    const uint8_t* pc = SWAP ? a.w_codes : a.x_codes;
+    const uint8_t* qc = SWAP ? a.x_codes : a.w_codes;
+    p.P = (int)(SWAP ? a.N : a.M);
+    p.Q = (int)(SWAP ? a.M : a.N);
+    p.sfp = SWAP ? a.w_scales : a.x_scales;
+    p.sfq = SWAP ? a.x_scales : a.w_scales;
+    p.x_is_p = SWAP ? 0 : 1;
+    p.p_tiles = (p.P + BP - 1) / BP;
+    p.q_tiles = (p.Q + TN - 1) / TN;
+    p.sfp_blocks = (p.P + 127) / 128;
+    p.sfq_blocks = (p.Q + 127) / 128;
+    CUtensorMap tp, tq;
+    if (!make_rows_code_map(&tp, pc, p.P, a.K, BP) || !make_rows_code_map(&tq, qc, p.Q, a.K, TN))
+        return FP4ATTN_ERR_CUDA;
+    auto kernel = gemm_fp4_kernel<TN, SWAP, SPLIT>;
+    constexpr size_t smem = (size_t)C::STAGE * C::STAGES + 1024;
+    static_assert(smem + sizeof(Bars) <= 227 * 1024, "shared memory budget");
+    static_assert(!SPLIT || (size_t)TN * BP * 4 <= (size_t)C::STAGE * C::STAGES, "the parts fit the ring");
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return FP4ATTN_ERR_CUDA;
+    const long long tiles = (long long)p.p_tiles * p.q_tiles;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * split : (tiles < sms ? tiles : sms)));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (SPLIT) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = (unsigned)split;
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (p.pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = (unsigned)n;
+    return cudaLaunchKernelEx(&cfg, kernel, tp, tq, p) == cudaSuccess ? FP4ATTN_OK : FP4ATTN_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_gemm_fp4(const GemmFp4Args& a, cudaStream_t stream) {
+    if (a.M == 0 || a.N == 0) return FP4ATTN_OK;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return FP4ATTN_ERR_CUDA;
+    GemmParams p{};
+    p.chunks = (int)scale_chunks(a.K);
+    p.stages = (p.chunks + CHUNKS - 1) / CHUNKS;
+    p.gx = a.gx;
+    p.gw = a.gw;
+    p.bias = a.bias;
+    p.out = a.out;
+    p.ld = a.ld;
+    p.N = (int)a.N;
+    p.pdl = a.after_quantize ? 1 : 0;
+    p.status = a.status;
+    const bool rows16 = (a.N & 7) == 0 && (a.ld & 7) == 0;
+    auto tiles = [&](int64_t P, int64_t Q, int tn) { return (P + 127) / 128 * ((Q + tn - 1) / tn); };
+    if (a.M <= 128) {
+        const int64_t t = tiles(a.N, a.M, 128);  // one tile per 128 weight rows
+        int split = 1;
+        while (split < 8 && t * split * 2 <= sms && split * 2 <= p.stages) split *= 2;
+        if (split > 1) {
+            if (a.M <= 16) return launch_one<16, true, true>(a, p, split, sms, stream);
+            if (a.M <= 64) return launch_one<64, true, true>(a, p, split, sms, stream);
+            return launch_one<128, true, true>(a, p, split, sms, stream);
+        }
+        if (a.M <= 16) return launch_one<16, true, false>(a, p, 1, sms, stream);
+        if (a.M <= 64) return launch_one<64, true, false>(a, p, 1, sms, stream);
+        return launch_one<128, true, false>(a, p, 1, sms, stream);
+    }
+    if (!rows16) {
+        if (tiles(a.N, a.M, 256) >= sms) return launch_one<256, true, false>(a, p, 1, sms, stream);
+        return launch_one<128, true, false>(a, p, 1, sms, stream);
+    }
+    if (tiles(a.M, a.N, 256) >= sms) return launch_one<256, false, false>(a, p, 1, sms, stream);
+    return launch_one<128, false, false>(a, p, 1, sms, stream);
+}
+
+}  // namespace fp4attn

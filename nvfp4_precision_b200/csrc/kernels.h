@@ -181,6 +181,56 @@ struct BwdArgs {
     int* status;
 };
 
+// ---- linear layers in NVFP4 (rows.cu, gemm.cu) ----
+
+// Parts of the largest-magnitude list and of a column sum, at most.
+constexpr int ROWS_AMAX_PARTS = 592;  // four CTAs on each of 148 SMs
+constexpr int COLSUM_PARTS = 128;
+
+// Workspace of the linear layer: [0,256) status word and spare, the computed
+// per-tensor scale at WS_GSCALE_OFFSET; the list of maxima; x's codes; x's
+// scale tiles.
+constexpr size_t WS_GSCALE_OFFSET = 64;
+inline size_t lws_part_offset() { return WS_STATUS_BYTES; }
+inline size_t lws_codes_offset() { return lws_part_offset() + ((size_t)ROWS_AMAX_PARTS * 4 + 255) / 256 * 256; }
+
+struct QuantRowsArgs {
+    const void* x;  // bf16 or fp32 [rows][K], row stride ld elements
+    int64_t ld, rows, K;
+    const float* g;  // device scalar or nullptr (1.0); ignored when dynamic
+    float* g_out;    // dynamic: receives the computed g
+    bool dynamic;
+    bool pdl;        // let the launch behind this one start early
+    float* part;     // dynamic: ROWS_AMAX_PARTS floats
+    int n_part;      // set by the launcher
+    uint8_t* codes;  // [rows][K/2]
+    uint8_t* scales; // tiles
+    int* status;
+};
+cudaError_t launch_quantize_rows(const QuantRowsArgs& a, bool f32, cudaStream_t stream);
+cudaError_t launch_dequant_rows(const uint8_t* codes, const uint8_t* scales, const float* g, int64_t rows, int64_t K,
+                                void* out, bool f32, cudaStream_t stream);
+// part: COLSUM_PARTS * cols floats
+cudaError_t launch_column_sums(const __nv_bfloat16* x, int64_t ld, int64_t rows, int64_t cols, float* part, float* out,
+                               cudaStream_t stream);
+
+// out[m][n] = g_x g_w sum_k x[m][k] w[n][k] + bias[n] over NVFP4 operands.
+struct GemmFp4Args {
+    const uint8_t* x_codes;
+    const uint8_t* x_scales;
+    const float* gx;
+    const uint8_t* w_codes;
+    const uint8_t* w_scales;
+    const float* gw;
+    const __nv_bfloat16* bias;  // [N] or nullptr
+    int64_t M, N, K;
+    __nv_bfloat16* out;
+    int64_t ld;
+    bool after_quantize;  // launched right behind the kernel that writes x: may start before it ends
+    int* status;
+};
+int launch_gemm_fp4(const GemmFp4Args& a, cudaStream_t stream);
+
 // Returns 0 on success, else an fp4attn_status code.
 int launch_backward(const BwdArgs& a, cudaStream_t stream);
 cudaError_t launch_dequant_bf16(const uint8_t* codes, const uint8_t* scales, const float* g, int64_t nblocks,

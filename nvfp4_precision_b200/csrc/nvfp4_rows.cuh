@@ -1,0 +1,68 @@
+// NVFP4 rows for the linear layers: the quantiser of one 16-value block and
+// the tile layout of the block scales, shared by the row quantiser and the
+// gated norm.
+#pragma once
+#include <cstdint>
+
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace fp4attn {
+
+// Scales of a matrix of `rows` x K values lie in tiles of 128 rows x 64
+// channels (four blocks), 512 bytes each, tiles of one row block in channel
+// order: the word of row r and 64-channel chunk c (its four scales) is word
+// 4 (r % 32) + (r % 128) / 32 of tile (r / 128) * chunks + c.  That is the
+// form in which tcgen05.cp takes scale factors, so the product copies tiles
+// from memory to TMEM without touching them; chunks = ceil(K / 64), and the
+// scales of channels past K are 0.
+__host__ __device__ inline int64_t scale_chunks(int64_t K) { return (K + 63) / 64; }
+__host__ __device__ inline int64_t scale_tile_bytes(int64_t rows, int64_t K) {
+    return (rows + 127) / 128 * scale_chunks(K) * 512;
+}
+__device__ __forceinline__ uint32_t scale_word_in_tile(uint32_t row_in_block) {
+    return 4u * (row_in_block & 31u) + (row_in_block >> 5);
+}
+
+// max(a, b) that keeps a NaN of either
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// Scale byte and reciprocal of one block with largest magnitude a:
+// s = E4M3(fl(fl(a / 6) / g)), inv = fl(1 / fl(g s)), 0 when s is 0.  The same
+// steps as the Q and K prologue's, so equal rows get equal bytes from both.
+__device__ __forceinline__ void row_block_scale(float a, float g, uint32_t& s, float& inv) {
+    float t = div6_rn(a);
+    if (g != 1.0f) t = __fdiv_rn(t, g);
+    s = cvt_e4m3(t) & 0x7Fu;
+    const float sd = ue4m3_value(s);
+    inv = (sd != 0.0f) ? __frcp_rn(__fmul_rn(g, sd)) : 0.0f;
+}
+
+// Codes of eight values times inv.
+__device__ __forceinline__ uint32_t row_codes8(const float (&v)[8], float inv) {
+    const float2 i2 = make_float2(inv, inv);
+    float2 r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r[k] = __fmul2_rn(make_float2(v[2 * k], v[2 * k + 1]), i2);
+    return cvt_e2m1x8(r[0].x, r[0].y, r[1].x, r[1].y, r[2].x, r[2].y, r[3].x, r[3].y);
+}
+
+// Smallest computed per-tensor scale and the value it covers.
+constexpr float kMinGscale = 5.421010862427522e-20f;  // 2^-64
+__device__ __forceinline__ float computed_gscale(float amax) {
+    // a NaN amax stays one (and is reported); fmaxf would drop it
+    const float g = __fdiv_rn(amax, 2688.0f);  // 6 * 448
+    return g < kMinGscale ? kMinGscale : g;
+}
+
+__device__ __forceinline__ bool bad_gscale(float g) { return !(g > 0.0f && g < INFINITY); }
+
+__device__ __forceinline__ void raise_status(int* status, int code) {
+    if (status) atomicCAS(status, 0, code);
+}
+
+}  // namespace fp4attn

@@ -30,12 +30,15 @@ ERR_WORKSPACE = 6
 NO_SMOOTH_K = 1
 NO_HADAMARD = 2
 DYNAMIC_GSCALE = 4
+BF16, F32 = 0, 1
 
 EXPORTS = (
     "fp4attn_workspace_bytes", "fp4attn_quantize_qk", "fp4attn_quantize_qk_ex", "fp4attn_quantize_qk_noalloc",
     "fp4attn_forward", "fp4attn_forward_ex", "fp4attn_forward_bf16qk", "fp4attn_forward_bf16qk_ex",
     "fp4attn_dequant", "fp4attn_dequant_bf16", "fp4attn_backward", "fp4attn_backward_ex",
     "fp4attn_backward_workspace_bytes",
+    "fp4attn_scale_tile_bytes", "fp4attn_linear_workspace_bytes", "fp4attn_quantize_rows", "fp4attn_dequant_rows",
+    "fp4attn_gemm", "fp4attn_linear",
     "fp4attn_read_status", "fp4attn_reset_status", "fp4attn_status_string", "fp4attn_encode_f32",
     "fp4attn_probe_qk_tile", "fp4attn_probe_pv_tile", "fp4attn_probe_wait_timeout", "fp4attn_probe_div6",
     "fp4attn_probe_withheld_key_sums", "fp4attn_probe_mma_rate",
@@ -94,6 +97,19 @@ def _load():
                                       P, ctypes.c_size_t, P]
     L.fp4attn_dequant.restype = ctypes.c_int
     L.fp4attn_dequant.argtypes = [P, P, P, Shape, P, P]
+    I32, SZ = ctypes.c_int, ctypes.c_size_t
+    L.fp4attn_scale_tile_bytes.restype = SZ
+    L.fp4attn_scale_tile_bytes.argtypes = [I64, I64]
+    L.fp4attn_linear_workspace_bytes.restype = SZ
+    L.fp4attn_linear_workspace_bytes.argtypes = [I64, I64, I64]
+    L.fp4attn_quantize_rows.restype = I32
+    L.fp4attn_quantize_rows.argtypes = [P, I32, I64, I64, I64, P, U32, P, P, P, SZ, P]
+    L.fp4attn_dequant_rows.restype = I32
+    L.fp4attn_dequant_rows.argtypes = [P, P, P, I64, I64, P, I32, P]
+    L.fp4attn_gemm.restype = I32
+    L.fp4attn_gemm.argtypes = [P, P, P, P, P, P, P, I64, I64, I64, P, I64, P, SZ, P]
+    L.fp4attn_linear.restype = I32
+    L.fp4attn_linear.argtypes = [P, I64, P, U32, P, P, P, P, I64, I64, I64, P, I64, P, SZ, P]
     L.fp4attn_read_status.restype = ctypes.c_int
     L.fp4attn_read_status.argtypes = [P, P, ctypes.POINTER(ctypes.c_int)]
     L.fp4attn_reset_status.restype = ctypes.c_int
@@ -371,6 +387,175 @@ def fp4_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, softmax_sca
     quantisation with a straight-through backward); dynamic_gscale selects the
     amax-derived per-tensor scales."""
     return FP4AttentionSTE.apply(q, k, v, softmax_scale, flags, dynamic_gscale)
+
+
+# ------------------------------------------------- linear layers in NVFP4 --
+
+def _check_device(t: torch.Tensor):
+    """The library launches on the current device: a tensor of another one
+    would be reached by address only, so it is refused."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensor on {t.device}: the library runs on the current CUDA device")
+
+
+def _type_of(t: torch.Tensor) -> int:
+    assert t.dtype in (torch.bfloat16, torch.float32), "rows are bf16 or fp32"
+    return F32 if t.dtype == torch.float32 else BF16
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    assert t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1), "rows must be contiguous"
+    return t.stride(0)
+
+
+def _check_packed(codes: torch.Tensor, scales: torch.Tensor, what: str):
+    """(rows, K) of packed NVFP4 rows."""
+    assert codes.dtype == torch.uint8 and codes.dim() == 2 and codes.is_contiguous(), f"{what}: codes are uint8 [rows, K/2]"
+    rows, K = codes.shape[0], 2 * codes.shape[1]
+    assert scales.dtype == torch.uint8 and scales.is_contiguous() \
+        and scales.numel() == lib.fp4attn_scale_tile_bytes(rows, K), f"{what}: scale tiles of [{rows}, {K}]"
+    _check_device(codes)
+    _check_device(scales)
+    return rows, K
+
+
+def _check_gscale(g: Optional[torch.Tensor]):
+    assert g is None or (g.dtype == torch.float32 and g.numel() == 1 and g.is_cuda), "a scale is one fp32 on the device"
+
+
+def fp4attn_scale_tile_bytes(rows: int, K: int) -> int:
+    return int(lib.fp4attn_scale_tile_bytes(rows, K))
+
+
+def fp4attn_linear_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(lib.fp4attn_linear_workspace_bytes(M, N, K))
+
+
+def new_linear_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
+    """A workspace of fp4attn_quantize_rows, fp4attn_gemm and fp4attn_linear
+    with a cleared status word; reusable for any call it is large enough for."""
+    ws = torch.empty(fp4attn_linear_workspace_bytes(M, N, K), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def tile_scales(scales: torch.Tensor) -> torch.Tensor:
+    """Row-major UE4M3 scales [rows, K/16] in the tile order of the linear
+    layers (a change of layout, done once for a weight)."""
+    rows, nb = scales.shape
+    R, C = -(-rows // 128), -(-nb // 4)
+    t = torch.zeros((R * 128, C * 4), dtype=torch.uint8, device=scales.device)
+    t[:rows, :nb] = scales
+    return t.view(R, 4, 32, C, 4).permute(0, 3, 2, 1, 4).reshape(-1)
+
+
+def untile_scales(scales: torch.Tensor, rows: int, K: int) -> torch.Tensor:
+    """The inverse of tile_scales: [rows, K/16]."""
+    R, C = -(-rows // 128), -(-K // 64)
+    t = scales.view(R, C, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(R * 128, C * 4)
+    return t[:rows, :K // 16].contiguous()
+
+
+def fp4attn_quantize_rows(x: torch.Tensor, gscale: Optional[torch.Tensor] = None, dynamic_gscale: bool = False,
+                          codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """NVFP4 rows of a bf16 or fp32 [rows, K] matrix (contiguous rows of any
+    stride that is a multiple of 8, or 4 for fp32).  dynamic_gscale=True
+    computes the per-tensor scale into gscale (allocated when None) instead of
+    reading it.  Returns dict(codes, scales, gscale, workspace)."""
+    _check_device(x)
+    _check_gscale(gscale)
+    rows, K = x.shape
+    dev = x.device
+    if codes is None:
+        codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=dev)
+    if scales is None:
+        scales = torch.empty(fp4attn_scale_tile_bytes(rows, K), dtype=torch.uint8, device=dev)
+    assert _check_packed(codes, scales, "output") == (rows, K) or K % 32
+    if workspace is None:
+        workspace = new_linear_workspace(0, 0, 32, dev)
+    if dynamic_gscale and gscale is None:
+        gscale = torch.empty(1, dtype=torch.float32, device=dev)
+    rc = lib.fp4attn_quantize_rows(_ptr(x), _type_of(x), _row_stride(x), rows, K, _ptr(gscale),
+                                   DYNAMIC_GSCALE if dynamic_gscale else 0, _ptr(codes), _ptr(scales),
+                                   _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(rc, "fp4attn_quantize_rows")
+    return dict(codes=codes, scales=scales, gscale=gscale, workspace=workspace)
+
+
+def fp4attn_dequant_rows(codes: torch.Tensor, scales: torch.Tensor, gscale: Optional[torch.Tensor] = None,
+                         dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """The values of packed NVFP4 rows, bf16 or fp32 [rows, K]."""
+    rows, K = _check_packed(codes, scales, "rows")
+    _check_gscale(gscale)
+    out = torch.empty((rows, K), dtype=dtype, device=codes.device)
+    rc = lib.fp4attn_dequant_rows(_ptr(codes), _ptr(scales), _ptr(gscale), rows, K, _ptr(out), _type_of(out),
+                                  _stream(stream))
+    _check(rc, "fp4attn_dequant_rows")
+    return out
+
+
+def _check_out(y: torch.Tensor, M: int, N: int):
+    assert y.shape == (M, N) and y.dtype == torch.bfloat16
+    _check_device(y)
+
+
+def _check_bias(bias: Optional[torch.Tensor], N: int):
+    if bias is not None:
+        assert bias.shape == (N,) and bias.dtype == torch.bfloat16 and bias.is_contiguous(), "bias is bf16 [N]"
+        _check_device(bias)
+
+
+def fp4attn_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+                 x_gscale: Optional[torch.Tensor] = None, w_gscale: Optional[torch.Tensor] = None,
+                 bias: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y = g_x g_w x w^T + bias of packed NVFP4 x [M, K] and w [N, K]: bf16
+    [M, N] (y may have any row stride)."""
+    M, K = _check_packed(x_codes, x_scales, "x")
+    N, K2 = _check_packed(w_codes, w_scales, "w")
+    assert K == K2, "x and w share K"
+    _check_gscale(x_gscale)
+    _check_gscale(w_gscale)
+    _check_bias(bias, N)
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=x_codes.device)
+    _check_out(y, M, N)
+    if workspace is None:
+        workspace = new_linear_workspace(0, 0, 32, x_codes.device)
+    rc = lib.fp4attn_gemm(_ptr(x_codes), _ptr(x_scales), _ptr(x_gscale), _ptr(w_codes), _ptr(w_scales),
+                          _ptr(w_gscale), _ptr(bias), M, N, K, _ptr(y), _row_stride(y), _ptr(workspace),
+                          workspace.numel(), _stream(stream))
+    _check(rc, "fp4attn_gemm")
+    return y
+
+
+def fp4attn_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+                   w_gscale: Optional[torch.Tensor] = None, x_gscale: Optional[torch.Tensor] = None,
+                   dynamic_gscale: bool = False, bias: Optional[torch.Tensor] = None,
+                   y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """The NVFP4 linear layer of bf16 x [M, K]: quantises x (per-tensor scale
+    x_gscale, None for 1, or computed with dynamic_gscale) and multiplies by
+    the packed weight [N, K].  bf16 [M, N]."""
+    assert x.dtype == torch.bfloat16, "x is bf16"
+    _check_device(x)
+    M, K = x.shape
+    N, K2 = _check_packed(w_codes, w_scales, "w")
+    assert K == K2, "x and w share K"
+    _check_gscale(x_gscale)
+    _check_gscale(w_gscale)
+    _check_bias(bias, N)
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    _check_out(y, M, N)
+    if workspace is None:
+        workspace = new_linear_workspace(M, N, K, x.device)
+    rc = lib.fp4attn_linear(_ptr(x), _row_stride(x), _ptr(x_gscale), DYNAMIC_GSCALE if dynamic_gscale else 0,
+                            _ptr(w_codes), _ptr(w_scales), _ptr(w_gscale), _ptr(bias), M, N, K, _ptr(y),
+                            _row_stride(y), _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(rc, "fp4attn_linear")
+    return y
 
 
 def fp4attn_read_status(workspace: torch.Tensor, stream=None) -> int:
