@@ -360,6 +360,85 @@ int fp4attn_linear(const void* x_bf16_dev, int64_t x_stride, float* x_gscale_dev
                    const void* bias_bf16_dev, int64_t M, int64_t N, int64_t K, void* y_bf16_dev, int64_t y_stride,
                    void* workspace_dev, size_t workspace_bytes, cudaStream_t stream);
 
+/* Straight-through gradients of fp4attn_linear: with x^ = g_x s e2m1 and w^ the
+ * values the forward multiplied,
+ *   dx = dy w^ [M, K] bf16,   dw = dy^T x^ [N, K] bf16,   dbias = sum_m dy [N] fp32.
+ *   dy_bf16_dev : [M, N], dy_stride a multiple of 8, at least N (N may be odd;
+ *     what lies behind a row's N values is not used).
+ *   x_codes, x_scales, x_gscale : the quantised input the forward kept
+ *     (fp4attn_quantize_rows); read for dw only.  w_*: read for dx only.
+ *   dx (dx_stride a multiple of 8, at least K), dw (contiguous), dbias: each
+ *     may be NULL and is not computed then.
+ * fp32 accumulation in an order that depends on the sizes and on which
+ * gradients are asked for only.  With M or N of 0 the sums over nothing are 0.
+ * Device errors: FP4ATTN_ERR_RANGE for a bad g, FP4ATTN_ERR_TIMEOUT. */
+size_t fp4attn_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int fp4attn_linear_backward(const void* dy_bf16_dev, int64_t dy_stride, const uint8_t* x_codes_dev,
+                            const uint8_t* x_scales_dev, const float* x_gscale_dev, const uint8_t* w_codes_dev,
+                            const uint8_t* w_scales_dev, const float* w_gscale_dev, int64_t M, int64_t N, int64_t K,
+                            void* dx_bf16_dev, int64_t dx_stride, void* dw_bf16_dev, float* dbias_dev,
+                            void* workspace_dev, size_t workspace_bytes, cudaStream_t stream);
+
+/* ---- the norms around a branch ---------------------------------------------
+ * What stands between a block's branch (attention or MLP, output h) and the
+ * next one (input z), on rows of C channels; rows of `groups` equal samples:
+ *   y = x + gate * (post_weight * norm(h))
+ *   z = norm(y) * pre_weight * (1 + scale) + shift
+ *   norm(v) = v / sqrt(mean(v^2) + eps); with FP4ATTN_LAYER_NORM the same of
+ *   v - mean(v)
+ * post_weight, pre_weight: bf16 [C]; gate, scale, shift: bf16 [groups, C] with
+ * row strides (multiples of 8, not read for one group), e.g. slices of a
+ * modulation layer's output.  NULL stands for 1, 1, 1, 0 and 0.
+ * C is a multiple of 8 up to 16384, rows up to 4194304, rows a multiple of
+ * groups, groups up to 1048576; eps >= 0.  Pointers are 16-byte aligned (fp32
+ * gradients of vectors: 4), row strides in elements, multiples of 8 (4 for
+ * fp32 rows), at least C, not read for one row. */
+enum { FP4ATTN_LAYER_NORM = 8u };
+
+typedef struct {
+    const void* post_weight;
+    const void* pre_weight;
+    const void* gate;
+    int64_t gate_stride;
+    const void* scale;
+    int64_t scale_stride;
+    const void* shift;
+    int64_t shift_stride;
+} fp4attn_norm_vectors;
+
+/* Forward, in fp32 from the inputs to one rounding of each output (z from the
+ * unrounded y).
+ *   x_dev : residual rows, bf16 or fp32 (x_type).  h_dev : bf16, or NULL for y = x.
+ *   y_dev : x's type; may be NULL, may be x itself (of the same stride).
+ *   z_dev : bf16, or NULL; or z_codes and z_scales: the NVFP4 rows of the bf16
+ *     z under the static scale z_gscale (NULL for 1), as fp4attn_quantize_rows
+ *     of it would write them (C a multiple of 32; scale bytes of rows past the
+ *     last are not written).
+ *   workspace_dev : as of fp4attn_gemm; may be NULL unless z is quantised (a
+ *     wait that runs out then leaves NaN rows as its only sign).
+ * Device errors: FP4ATTN_ERR_RANGE for a non-finite z or a bad g (quantised z
+ * only), FP4ATTN_ERR_TIMEOUT. */
+int fp4attn_norm_gate(const void* x_dev, int x_type, int64_t x_stride, const void* h_bf16_dev, int64_t h_stride,
+                      const fp4attn_norm_vectors* vectors, int64_t rows, int64_t C, int64_t groups, float eps,
+                      uint32_t flags, void* y_dev, int64_t y_stride, void* z_bf16_dev, int64_t z_stride,
+                      uint8_t* z_codes_dev, uint8_t* z_scales_dev, const float* z_gscale_dev, void* workspace_dev,
+                      size_t workspace_bytes, cudaStream_t stream);
+
+/* Gradients for dz (bf16) and dy (y's type, NULL for 0), from the forward's y
+ * and h (NULL as in the forward; dh, dgate, dpost_weight are then NULL too):
+ *   dx (y's type; the residual's gradient), dh (bf16), and in fp32 dshift,
+ *   dscale, dgate [groups, C], dpre_weight, dpost_weight [C] (each may be NULL).
+ * dx may be dy, dh may be dz or h, of the same strides.  Sums down the rows are added in a
+ * fixed order.  Device errors: FP4ATTN_ERR_TIMEOUT. */
+size_t fp4attn_norm_gate_backward_workspace_bytes(int64_t rows, int64_t C, int64_t groups);
+int fp4attn_norm_gate_backward(const void* dz_bf16_dev, int64_t dz_stride, const void* dy_dev, int64_t dy_stride,
+                               const void* y_dev, int64_t y_stride, int y_type, const void* h_bf16_dev,
+                               int64_t h_stride, const fp4attn_norm_vectors* vectors, int64_t rows, int64_t C,
+                               int64_t groups, float eps, uint32_t flags, void* dx_dev, int64_t dx_stride,
+                               void* dh_bf16_dev, int64_t dh_stride, float* dshift_dev, float* dscale_dev,
+                               float* dgate_dev, float* dpre_weight_dev, float* dpost_weight_dev, void* workspace_dev,
+                               size_t workspace_bytes, cudaStream_t stream);
+
 /* Read (synchronously: waits for the stream) and return in *device_status the
  * workspace status word: FP4ATTN_OK or the first device error. */
 int fp4attn_read_status(const void* workspace_dev, cudaStream_t stream, int* device_status);

@@ -231,6 +231,87 @@ struct GemmFp4Args {
 };
 int launch_gemm_fp4(const GemmFp4Args& a, cudaStream_t stream);
 
+// Its straight-through gradients (linear_bwd.cu).
+struct LinearBwdArgs {
+    const __nv_bfloat16* dy;
+    int64_t ld_dy;
+    const uint8_t* x_codes;
+    const uint8_t* x_scales;
+    const float* gx;
+    const uint8_t* w_codes;
+    const uint8_t* w_scales;
+    const float* gw;
+    int64_t M, N, K;
+    __nv_bfloat16* dx;  // [M][K], may be nullptr
+    int64_t ld_dx;
+    __nv_bfloat16* dw;  // [N][K], may be nullptr
+    float* dbias;       // [N], may be nullptr
+    // workspace
+    __nv_bfloat16* w_bf16;  // [N][K]
+    __nv_bfloat16* x_bf16;  // [M][K]
+    float* colsum_part;     // COLSUM_PARTS * N
+    float* part;            // linear_backward_part_bytes
+    int* status;
+};
+size_t linear_backward_part_bytes(int64_t M, int64_t N, int64_t K);
+int launch_linear_backward(const LinearBwdArgs& a, cudaStream_t stream);
+
+// ---- the norms around a branch (norm.cu) ----
+
+struct NormArgs {
+    const void* x;  // residual, bf16 or fp32 [rows][C]
+    int64_t ldx;
+    const __nv_bfloat16* h;  // branch, or nullptr: y = x
+    int64_t ldh;
+    const __nv_bfloat16 *post, *gate, *pre, *scale, *shift;  // [C] or [groups][C]; nullptr: 1, 1, 1, 0, 0
+    int64_t lgate, lscale, lshift;
+    int64_t rows, rows_per_group;
+    int C;
+    float eps;
+    bool layer;
+    bool pdl;           // let the launch behind this one start early
+    void* y;            // may be nullptr
+    int64_t ldy;
+    __nv_bfloat16* z;   // may be nullptr
+    int64_t ldz;
+    uint8_t* codes;     // z as NVFP4 rows instead
+    uint8_t* scales;
+    const float* gz;
+    int64_t chunks;
+    int* status;        // may be nullptr
+    int slots;          // set by the launcher
+    uint32_t slot_bytes;
+};
+int launch_norm_gate(const NormArgs& a, bool f32, cudaStream_t stream);
+
+struct NormBwdArgs {
+    const __nv_bfloat16* dz;
+    int64_t lddz;
+    const void* dy;  // may be nullptr: 0
+    int64_t lddy;
+    const void* y;
+    int64_t ldy;
+    const __nv_bfloat16* h;  // may be nullptr: y = x
+    int64_t ldh;
+    const __nv_bfloat16 *post, *gate, *pre, *scale;
+    int64_t lgate, lscale;
+    int64_t rows, rows_per_group, groups, parts;
+    int C;
+    float eps;
+    bool layer;
+    void* dx;
+    int64_t lddx;
+    __nv_bfloat16* dh;
+    int64_t lddh;
+    float *dshift, *dscale, *dgate, *dpre, *dpost;  // [groups][C], [C]; each may be nullptr
+    float* part;  // groups * parts * 3 * C
+    int* status;
+    int slots;  // set by the launcher
+    uint32_t slot_bytes;
+};
+int64_t norm_backward_parts(int64_t rows, int64_t C, int64_t groups);
+int launch_norm_gate_backward(const NormBwdArgs& a, bool f32, cudaStream_t stream);
+
 // Returns 0 on success, else an fp4attn_status code.
 int launch_backward(const BwdArgs& a, cudaStream_t stream);
 cudaError_t launch_dequant_bf16(const uint8_t* codes, const uint8_t* scales, const float* g, int64_t nblocks,

@@ -46,6 +46,35 @@ int clear_error(int st) {
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
+// Workspace of the linear layer's backward: [0,256) status word and spare; W~
+// and X~ in bf16; partial column sums of dy; parts of split tiles.
+size_t lbws_x_offset(int64_t N, int64_t K) { return WS_STATUS_BYTES + round256((size_t)(N * K) * 2); }
+size_t lbws_colsum_offset(int64_t M, int64_t N, int64_t K) { return lbws_x_offset(N, K) + round256((size_t)(M * K) * 2); }
+size_t lbws_part_offset(int64_t M, int64_t N, int64_t K) {
+    return lbws_colsum_offset(M, N, K) + round256((size_t)N * COLSUM_PARTS * 4);
+}
+
+constexpr int64_t kMaxC = 16384;
+constexpr int64_t kMaxGroups = 1048576;
+
+int check_norm_sizes(int64_t rows, int64_t C, int64_t groups) {
+    if (rows < 0 || C <= 0 || groups <= 0 || rows % groups) return FP4ATTN_ERR_INVALID_ARG;
+    return (rows > kMaxRows || C % 8 || C > kMaxC || groups > kMaxGroups) ? FP4ATTN_ERR_UNSUPPORTED : FP4ATTN_OK;
+}
+// A row matrix: 16-byte aligned, rows a multiple of `unit` elements apart.
+bool bad_rows(const void* p, int64_t ld, int64_t rows, int64_t C, int64_t unit) {
+    return !aligned16(p) || (rows > 1 && (ld < C || ld % unit || ld >= kMaxStride));
+}
+bool bad_vector(const void* p, int64_t ld, int64_t groups, int64_t C) {
+    return !aligned16(p) || (p && groups > 1 && (ld < C || ld % 8 || ld >= kMaxStride));
+}
+int check_norm_vectors(const fp4attn_norm_vectors& v, int64_t groups, int64_t C) {
+    return (!aligned16(v.post_weight) || !aligned16(v.pre_weight) || bad_vector(v.gate, v.gate_stride, groups, C) ||
+            bad_vector(v.scale, v.scale_stride, groups, C) || bad_vector(v.shift, v.shift_stride, groups, C))
+               ? FP4ATTN_ERR_INVALID_ARG
+               : FP4ATTN_OK;
+}
+
 }  // namespace
 
 }  // namespace fp4attn
@@ -188,6 +217,185 @@ int fp4attn_linear(const void* x, int64_t x_stride, float* gx, uint32_t flags, c
     a.after_quantize = true;
     a.status = q.status;
     return clear_error(launch_gemm_fp4(a, stream));
+}
+
+size_t fp4attn_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (check_mnk(M, N, K) != FP4ATTN_OK) return WS_STATUS_BYTES;
+    return lbws_part_offset(M, N, K) + round256(linear_backward_part_bytes(M, N, K));
+}
+
+int fp4attn_linear_backward(const void* dy, int64_t dy_stride, const uint8_t* x_codes, const uint8_t* x_scales,
+                            const float* gx, const uint8_t* w_codes, const uint8_t* w_scales, const float* gw, int64_t M,
+                            int64_t N, int64_t K, void* dx, int64_t dx_stride, void* dw, float* dbias, void* workspace,
+                            size_t workspace_bytes, cudaStream_t stream) {
+    const int st = check_mnk(M, N, K);
+    if (st != FP4ATTN_OK) return st;
+    if (!good(workspace) || workspace_bytes < fp4attn_linear_backward_workspace_bytes(M, N, K))
+        return FP4ATTN_ERR_WORKSPACE;
+    if (!aligned4(gx) || !aligned4(gw) || !aligned4(dbias)) return FP4ATTN_ERR_INVALID_ARG;
+    if (dx && M > 0 && bad_rows(dx, dx_stride, M, K, 8)) return FP4ATTN_ERR_INVALID_ARG;
+    if (!aligned16(dw)) return FP4ATTN_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) {
+        // sums over nothing
+        cudaError_t e = cudaSuccess;
+        if (dx && M > 0)
+            e = cudaMemset2DAsync(dx, (size_t)(M > 1 ? dx_stride : K) * 2, 0, (size_t)K * 2, (size_t)M, stream);
+        if (e == cudaSuccess && dw && N > 0) e = cudaMemsetAsync(dw, 0, (size_t)(N * K) * 2, stream);
+        if (e == cudaSuccess && dbias && N > 0) e = cudaMemsetAsync(dbias, 0, (size_t)N * 4, stream);
+        return launch_status(e);
+    }
+    if (!dy || bad_rows(dy, dy_stride, M, N, 8)) return FP4ATTN_ERR_INVALID_ARG;
+    if (dx && (!good(w_codes) || !good(w_scales))) return FP4ATTN_ERR_INVALID_ARG;
+    if (dw && (!good(x_codes) || !good(x_scales))) return FP4ATTN_ERR_INVALID_ARG;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    LinearBwdArgs a{};
+    a.dy = static_cast<const __nv_bfloat16*>(dy);
+    a.ld_dy = M > 1 ? dy_stride : (N + 7) / 8 * 8;
+    a.x_codes = x_codes;
+    a.x_scales = x_scales;
+    a.gx = gx;
+    a.w_codes = w_codes;
+    a.w_scales = w_scales;
+    a.gw = gw;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.dx = static_cast<__nv_bfloat16*>(dx);
+    a.ld_dx = M > 1 ? dx_stride : K;
+    a.dw = static_cast<__nv_bfloat16*>(dw);
+    a.dbias = dbias;
+    a.w_bf16 = reinterpret_cast<__nv_bfloat16*>(ws + WS_STATUS_BYTES);
+    a.x_bf16 = reinterpret_cast<__nv_bfloat16*>(ws + lbws_x_offset(N, K));
+    a.colsum_part = reinterpret_cast<float*>(ws + lbws_colsum_offset(M, N, K));
+    a.part = reinterpret_cast<float*>(ws + lbws_part_offset(M, N, K));
+    a.status = static_cast<int*>(workspace);
+    return clear_error(launch_linear_backward(a, stream));
+}
+
+int fp4attn_norm_gate(const void* x, int x_type, int64_t x_stride, const void* h, int64_t h_stride,
+                      const fp4attn_norm_vectors* vectors, int64_t rows, int64_t C, int64_t groups, float eps,
+                      uint32_t flags, void* y, int64_t y_stride, void* z, int64_t z_stride, uint8_t* z_codes,
+                      uint8_t* z_scales, const float* z_gscale, void* workspace, size_t workspace_bytes,
+                      cudaStream_t stream) {
+    int st = check_norm_sizes(rows, C, groups);
+    if (st != FP4ATTN_OK) return st;
+    const bool quant = z_codes || z_scales;
+    if (!vectors || (x_type != FP4ATTN_BF16 && x_type != FP4ATTN_F32) || (flags & ~(uint32_t)FP4ATTN_LAYER_NORM) ||
+        !(eps >= 0.0f && eps <= 3.0e38f))
+        return FP4ATTN_ERR_INVALID_ARG;
+    if (quant && (!z_codes || !z_scales || z || !aligned4(z_gscale))) return FP4ATTN_ERR_INVALID_ARG;
+    if (quant && C % 32) return FP4ATTN_ERR_UNSUPPORTED;
+    if (workspace ? (!good(workspace) || workspace_bytes < lws_codes_offset()) : quant) return FP4ATTN_ERR_WORKSPACE;
+    if (rows == 0) return FP4ATTN_OK;
+    st = check_norm_vectors(*vectors, groups, C);
+    if (st != FP4ATTN_OK) return st;
+    const int64_t unit = x_type == FP4ATTN_F32 ? 4 : 8;
+    if (!x || (!y && !z && !quant) || bad_rows(x, x_stride, rows, C, unit) || bad_rows(h, h ? h_stride : C, rows, C, 8) ||
+        bad_rows(y, y ? y_stride : C, rows, C, unit) || bad_rows(z, z ? z_stride : C, rows, C, 8) ||
+        !aligned16(z_codes) || !aligned16(z_scales))
+        return FP4ATTN_ERR_INVALID_ARG;
+    NormArgs a{};
+    a.x = x;
+    a.ldx = x_stride;
+    a.h = static_cast<const __nv_bfloat16*>(h);
+    a.ldh = h_stride;
+    a.post = static_cast<const __nv_bfloat16*>(vectors->post_weight);
+    a.gate = static_cast<const __nv_bfloat16*>(vectors->gate);
+    a.pre = static_cast<const __nv_bfloat16*>(vectors->pre_weight);
+    a.scale = static_cast<const __nv_bfloat16*>(vectors->scale);
+    a.shift = static_cast<const __nv_bfloat16*>(vectors->shift);
+    a.lgate = vectors->gate_stride;
+    a.lscale = vectors->scale_stride;
+    a.lshift = vectors->shift_stride;
+    a.rows = rows;
+    a.rows_per_group = rows / groups;
+    a.C = (int)C;
+    a.eps = eps;
+    a.layer = (flags & FP4ATTN_LAYER_NORM) != 0;
+    a.y = y;
+    a.ldy = y_stride;
+    a.z = static_cast<__nv_bfloat16*>(z);
+    a.ldz = z_stride;
+    a.codes = z_codes;
+    a.scales = z_scales;
+    a.gz = z_gscale;
+    a.chunks = scale_chunks(C);
+    a.status = static_cast<int*>(workspace);
+    return clear_error(launch_norm_gate(a, x_type == FP4ATTN_F32, stream));
+}
+
+size_t fp4attn_norm_gate_backward_workspace_bytes(int64_t rows, int64_t C, int64_t groups) {
+    if (check_norm_sizes(rows, C, groups) != FP4ATTN_OK) return WS_STATUS_BYTES;
+    return WS_STATUS_BYTES + round256((size_t)(groups * norm_backward_parts(rows, C, groups)) * 3 * (size_t)C * 4);
+}
+
+int fp4attn_norm_gate_backward(const void* dz, int64_t dz_stride, const void* dy, int64_t dy_stride, const void* y,
+                               int64_t y_stride, int y_type, const void* h, int64_t h_stride,
+                               const fp4attn_norm_vectors* vectors, int64_t rows, int64_t C, int64_t groups, float eps,
+                               uint32_t flags, void* dx, int64_t dx_stride, void* dh, int64_t dh_stride, float* dshift,
+                               float* dscale, float* dgate, float* dpre_weight, float* dpost_weight, void* workspace,
+                               size_t workspace_bytes, cudaStream_t stream) {
+    int st = check_norm_sizes(rows, C, groups);
+    if (st != FP4ATTN_OK) return st;
+    if (!vectors || (y_type != FP4ATTN_BF16 && y_type != FP4ATTN_F32) || (flags & ~(uint32_t)FP4ATTN_LAYER_NORM) ||
+        !(eps >= 0.0f && eps <= 3.0e38f))
+        return FP4ATTN_ERR_INVALID_ARG;
+    if (!good(workspace) || workspace_bytes < fp4attn_norm_gate_backward_workspace_bytes(rows, C, groups))
+        return FP4ATTN_ERR_WORKSPACE;
+    if (!aligned4(dshift) || !aligned4(dscale) || !aligned4(dgate) || !aligned4(dpre_weight) || !aligned4(dpost_weight))
+        return FP4ATTN_ERR_INVALID_ARG;
+    if (!h && (rows > 0 && (dh || dgate || dpost_weight))) return FP4ATTN_ERR_INVALID_ARG;
+    if (rows == 0) {
+        float* const per_group[3] = {dshift, dscale, dgate};
+        float* const weights[2] = {dpre_weight, dpost_weight};
+        cudaError_t e = cudaSuccess;
+        for (float* p : per_group)
+            if (p && e == cudaSuccess) e = cudaMemsetAsync(p, 0, (size_t)(groups * C) * 4, stream);
+        for (float* p : weights)
+            if (p && e == cudaSuccess) e = cudaMemsetAsync(p, 0, (size_t)C * 4, stream);
+        return launch_status(e);
+    }
+    st = check_norm_vectors(*vectors, groups, C);
+    if (st != FP4ATTN_OK) return st;
+    const int64_t unit = y_type == FP4ATTN_F32 ? 4 : 8;
+    if (!dz || !y || !dx || (h && !dh) || bad_rows(dz, dz_stride, rows, C, 8) || bad_rows(dy, dy ? dy_stride : C, rows, C, unit) ||
+        bad_rows(y, y_stride, rows, C, unit) || bad_rows(h, h ? h_stride : C, rows, C, 8) ||
+        bad_rows(dx, dx_stride, rows, C, unit) || bad_rows(dh, dh ? dh_stride : C, rows, C, 8))
+        return FP4ATTN_ERR_INVALID_ARG;
+    NormBwdArgs a{};
+    a.dz = static_cast<const __nv_bfloat16*>(dz);
+    a.lddz = dz_stride;
+    a.dy = dy;
+    a.lddy = dy_stride;
+    a.y = y;
+    a.ldy = y_stride;
+    a.h = static_cast<const __nv_bfloat16*>(h);
+    a.ldh = h_stride;
+    a.post = static_cast<const __nv_bfloat16*>(vectors->post_weight);
+    a.gate = static_cast<const __nv_bfloat16*>(vectors->gate);
+    a.pre = static_cast<const __nv_bfloat16*>(vectors->pre_weight);
+    a.scale = static_cast<const __nv_bfloat16*>(vectors->scale);
+    a.lgate = vectors->gate_stride;
+    a.lscale = vectors->scale_stride;
+    a.rows = rows;
+    a.rows_per_group = rows / groups;
+    a.groups = groups;
+    a.parts = norm_backward_parts(rows, C, groups);
+    a.C = (int)C;
+    a.eps = eps;
+    a.layer = (flags & FP4ATTN_LAYER_NORM) != 0;
+    a.dx = dx;
+    a.lddx = dx_stride;
+    a.dh = static_cast<__nv_bfloat16*>(dh);
+    a.lddh = dh_stride;
+    a.dshift = dshift;
+    a.dscale = dscale;
+    a.dgate = dgate;
+    a.dpre = dpre_weight;
+    a.dpost = dpost_weight;
+    a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + WS_STATUS_BYTES);
+    a.status = static_cast<int*>(workspace);
+    return clear_error(launch_norm_gate_backward(a, y_type == FP4ATTN_F32, stream));
 }
 
 }  // extern "C"

@@ -8,6 +8,7 @@ no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -30,6 +31,7 @@ ERR_WORKSPACE = 6
 NO_SMOOTH_K = 1
 NO_HADAMARD = 2
 DYNAMIC_GSCALE = 4
+LAYER_NORM = 8
 BF16, F32 = 0, 1
 
 EXPORTS = (
@@ -38,7 +40,8 @@ EXPORTS = (
     "fp4attn_dequant", "fp4attn_dequant_bf16", "fp4attn_backward", "fp4attn_backward_ex",
     "fp4attn_backward_workspace_bytes",
     "fp4attn_scale_tile_bytes", "fp4attn_linear_workspace_bytes", "fp4attn_quantize_rows", "fp4attn_dequant_rows",
-    "fp4attn_gemm", "fp4attn_linear",
+    "fp4attn_gemm", "fp4attn_linear", "fp4attn_linear_backward_workspace_bytes", "fp4attn_linear_backward",
+    "fp4attn_norm_gate", "fp4attn_norm_gate_backward_workspace_bytes", "fp4attn_norm_gate_backward",
     "fp4attn_read_status", "fp4attn_reset_status", "fp4attn_status_string", "fp4attn_encode_f32",
     "fp4attn_probe_qk_tile", "fp4attn_probe_pv_tile", "fp4attn_probe_wait_timeout", "fp4attn_probe_div6",
     "fp4attn_probe_withheld_key_sums", "fp4attn_probe_mma_rate",
@@ -52,6 +55,13 @@ class Shape(ctypes.Structure):
 class Strides(ctypes.Structure):
     """Element strides (b, h, n) of a [B,H,N,128] tensor whose channels are contiguous."""
     _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("n", ctypes.c_int64)]
+
+
+class NormVectors(ctypes.Structure):
+    _fields_ = [("post_weight", ctypes.c_void_p), ("pre_weight", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("gate_stride", ctypes.c_int64),
+                ("scale", ctypes.c_void_p), ("scale_stride", ctypes.c_int64),
+                ("shift", ctypes.c_void_p), ("shift_stride", ctypes.c_int64)]
 
 
 class Fp4AttnError(RuntimeError):
@@ -110,6 +120,19 @@ def _load():
     L.fp4attn_gemm.argtypes = [P, P, P, P, P, P, P, I64, I64, I64, P, I64, P, SZ, P]
     L.fp4attn_linear.restype = I32
     L.fp4attn_linear.argtypes = [P, I64, P, U32, P, P, P, P, I64, I64, I64, P, I64, P, SZ, P]
+    L.fp4attn_linear_backward_workspace_bytes.restype = SZ
+    L.fp4attn_linear_backward_workspace_bytes.argtypes = [I64, I64, I64]
+    L.fp4attn_linear_backward.restype = I32
+    L.fp4attn_linear_backward.argtypes = [P, I64, P, P, P, P, P, P, I64, I64, I64, P, I64, P, P, P, SZ, P]
+    VEC = ctypes.POINTER(NormVectors)
+    L.fp4attn_norm_gate.restype = I32
+    L.fp4attn_norm_gate.argtypes = [P, I32, I64, P, I64, VEC, I64, I64, I64, ctypes.c_float, U32, P, I64, P, I64, P, P,
+                                    P, P, SZ, P]
+    L.fp4attn_norm_gate_backward_workspace_bytes.restype = SZ
+    L.fp4attn_norm_gate_backward_workspace_bytes.argtypes = [I64, I64, I64]
+    L.fp4attn_norm_gate_backward.restype = I32
+    L.fp4attn_norm_gate_backward.argtypes = [P, I64, P, I64, P, I64, I32, P, I64, VEC, I64, I64, I64, ctypes.c_float,
+                                             U32, P, I64, P, I64, P, P, P, P, P, P, SZ, P]
     L.fp4attn_read_status.restype = ctypes.c_int
     L.fp4attn_read_status.argtypes = [P, P, ctypes.POINTER(ctypes.c_int)]
     L.fp4attn_reset_status.restype = ctypes.c_int
@@ -398,6 +421,20 @@ def _check_device(t: torch.Tensor):
         raise ValueError(f"tensor on {t.device}: the library runs on the current CUDA device")
 
 
+def _on_stream(fn):
+    """Runs a call given ``stream`` with that stream as the current one, so
+    that what it allocates (outputs, a workspace) is ordered there too."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return fn(*args, **kwargs)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(stream):
+            return fn(*args, **kwargs)
+    return call
+
+
 def _type_of(t: torch.Tensor) -> int:
     assert t.dtype in (torch.bfloat16, torch.float32), "rows are bf16 or fp32"
     return F32 if t.dtype == torch.float32 else BF16
@@ -420,7 +457,19 @@ def _check_packed(codes: torch.Tensor, scales: torch.Tensor, what: str):
 
 
 def _check_gscale(g: Optional[torch.Tensor]):
-    assert g is None or (g.dtype == torch.float32 and g.numel() == 1 and g.is_cuda), "a scale is one fp32 on the device"
+    if g is not None:
+        assert g.dtype == torch.float32 and g.numel() == 1, "a scale is one fp32 on the device"
+        _check_device(g)
+
+
+def _check_workspace(ws: torch.Tensor):
+    assert ws.dtype == torch.uint8 and ws.is_contiguous(), "a workspace is contiguous uint8"
+    _check_device(ws)
+
+
+def _check_rows(t: torch.Tensor, rows: int, cols: int, dtype: torch.dtype, what: str):
+    assert t.shape == (rows, cols) and t.dtype == dtype, f"{what}: {dtype} [{rows}, {cols}]"
+    _check_device(t)
 
 
 def fp4attn_scale_tile_bytes(rows: int, K: int) -> int:
@@ -431,12 +480,25 @@ def fp4attn_linear_workspace_bytes(M: int, N: int, K: int) -> int:
     return int(lib.fp4attn_linear_workspace_bytes(M, N, K))
 
 
-def new_linear_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
-    """A workspace of fp4attn_quantize_rows, fp4attn_gemm and fp4attn_linear
-    with a cleared status word; reusable for any call it is large enough for."""
-    ws = torch.empty(fp4attn_linear_workspace_bytes(M, N, K), dtype=torch.uint8, device=device)
+def _status_workspace(nbytes: int, device) -> torch.Tensor:
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     ws[:256].zero_()
     return ws
+
+
+def new_linear_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
+    """A workspace of fp4attn_quantize_rows, fp4attn_gemm, fp4attn_linear and
+    fp4attn_norm_gate with a cleared status word; reusable for any call it is
+    large enough for."""
+    return _status_workspace(fp4attn_linear_workspace_bytes(M, N, K), device)
+
+
+def new_linear_backward_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
+    return _status_workspace(int(lib.fp4attn_linear_backward_workspace_bytes(M, N, K)), device)
+
+
+def new_norm_backward_workspace(rows: int, C: int, groups: int = 1, device="cuda") -> torch.Tensor:
+    return _status_workspace(int(lib.fp4attn_norm_gate_backward_workspace_bytes(rows, C, groups)), device)
 
 
 def tile_scales(scales: torch.Tensor) -> torch.Tensor:
@@ -456,9 +518,10 @@ def untile_scales(scales: torch.Tensor, rows: int, K: int) -> torch.Tensor:
     return t[:rows, :K // 16].contiguous()
 
 
+@_on_stream
 def fp4attn_quantize_rows(x: torch.Tensor, gscale: Optional[torch.Tensor] = None, dynamic_gscale: bool = False,
                           codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
-                          workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+                          workspace: Optional[torch.Tensor] = None) -> dict:
     """NVFP4 rows of a bf16 or fp32 [rows, K] matrix (contiguous rows of any
     stride that is a multiple of 8, or 4 for fp32).  dynamic_gscale=True
     computes the per-tensor scale into gscale (allocated when None) instead of
@@ -474,30 +537,27 @@ def fp4attn_quantize_rows(x: torch.Tensor, gscale: Optional[torch.Tensor] = None
     assert _check_packed(codes, scales, "output") == (rows, K) or K % 32
     if workspace is None:
         workspace = new_linear_workspace(0, 0, 32, dev)
+    _check_workspace(workspace)
     if dynamic_gscale and gscale is None:
         gscale = torch.empty(1, dtype=torch.float32, device=dev)
     rc = lib.fp4attn_quantize_rows(_ptr(x), _type_of(x), _row_stride(x), rows, K, _ptr(gscale),
                                    DYNAMIC_GSCALE if dynamic_gscale else 0, _ptr(codes), _ptr(scales),
-                                   _ptr(workspace), workspace.numel(), _stream(stream))
+                                   _ptr(workspace), workspace.numel(), _stream(None))
     _check(rc, "fp4attn_quantize_rows")
     return dict(codes=codes, scales=scales, gscale=gscale, workspace=workspace)
 
 
+@_on_stream
 def fp4attn_dequant_rows(codes: torch.Tensor, scales: torch.Tensor, gscale: Optional[torch.Tensor] = None,
-                         dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+                         dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """The values of packed NVFP4 rows, bf16 or fp32 [rows, K]."""
     rows, K = _check_packed(codes, scales, "rows")
     _check_gscale(gscale)
     out = torch.empty((rows, K), dtype=dtype, device=codes.device)
     rc = lib.fp4attn_dequant_rows(_ptr(codes), _ptr(scales), _ptr(gscale), rows, K, _ptr(out), _type_of(out),
-                                  _stream(stream))
+                                  _stream(None))
     _check(rc, "fp4attn_dequant_rows")
     return out
-
-
-def _check_out(y: torch.Tensor, M: int, N: int):
-    assert y.shape == (M, N) and y.dtype == torch.bfloat16
-    _check_device(y)
 
 
 def _check_bias(bias: Optional[torch.Tensor], N: int):
@@ -506,10 +566,11 @@ def _check_bias(bias: Optional[torch.Tensor], N: int):
         _check_device(bias)
 
 
+@_on_stream
 def fp4attn_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
                  x_gscale: Optional[torch.Tensor] = None, w_gscale: Optional[torch.Tensor] = None,
                  bias: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
-                 workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y = g_x g_w x w^T + bias of packed NVFP4 x [M, K] and w [N, K]: bf16
     [M, N] (y may have any row stride)."""
     M, K = _check_packed(x_codes, x_scales, "x")
@@ -520,21 +581,22 @@ def fp4attn_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.T
     _check_bias(bias, N)
     if y is None:
         y = torch.empty((M, N), dtype=torch.bfloat16, device=x_codes.device)
-    _check_out(y, M, N)
+    _check_rows(y, M, N, torch.bfloat16, "y")
     if workspace is None:
         workspace = new_linear_workspace(0, 0, 32, x_codes.device)
+    _check_workspace(workspace)
     rc = lib.fp4attn_gemm(_ptr(x_codes), _ptr(x_scales), _ptr(x_gscale), _ptr(w_codes), _ptr(w_scales),
                           _ptr(w_gscale), _ptr(bias), M, N, K, _ptr(y), _row_stride(y), _ptr(workspace),
-                          workspace.numel(), _stream(stream))
+                          workspace.numel(), _stream(None))
     _check(rc, "fp4attn_gemm")
     return y
 
 
+@_on_stream
 def fp4attn_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
                    w_gscale: Optional[torch.Tensor] = None, x_gscale: Optional[torch.Tensor] = None,
                    dynamic_gscale: bool = False, bias: Optional[torch.Tensor] = None,
-                   y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                   stream=None) -> torch.Tensor:
+                   y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The NVFP4 linear layer of bf16 x [M, K]: quantises x (per-tensor scale
     x_gscale, None for 1, or computed with dynamic_gscale) and multiplies by
     the packed weight [N, K].  bf16 [M, N]."""
@@ -548,14 +610,152 @@ def fp4attn_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tenso
     _check_bias(bias, N)
     if y is None:
         y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    _check_out(y, M, N)
+    _check_rows(y, M, N, torch.bfloat16, "y")
     if workspace is None:
         workspace = new_linear_workspace(M, N, K, x.device)
+    _check_workspace(workspace)
     rc = lib.fp4attn_linear(_ptr(x), _row_stride(x), _ptr(x_gscale), DYNAMIC_GSCALE if dynamic_gscale else 0,
                             _ptr(w_codes), _ptr(w_scales), _ptr(w_gscale), _ptr(bias), M, N, K, _ptr(y),
-                            _row_stride(y), _ptr(workspace), workspace.numel(), _stream(stream))
+                            _row_stride(y), _ptr(workspace), workspace.numel(), _stream(None))
     _check(rc, "fp4attn_linear")
     return y
+
+
+@_on_stream
+def fp4attn_linear_backward(dy: torch.Tensor, x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.Tensor,
+                            w_scales: torch.Tensor, x_gscale: Optional[torch.Tensor] = None,
+                            w_gscale: Optional[torch.Tensor] = None, want_dx: bool = True, want_dw: bool = True,
+                            want_dbias: bool = True, workspace: Optional[torch.Tensor] = None):
+    """Straight-through gradients of fp4attn_linear for bf16 dy [M, N] and the
+    packed operands of the forward: (dx bf16 [M, K], dw bf16 [N, K], dbias
+    fp32 [N]), None in the place of one not wanted."""
+    M, K = _check_packed(x_codes, x_scales, "x")
+    N, K2 = _check_packed(w_codes, w_scales, "w")
+    assert K == K2, "x and w share K"
+    _check_rows(dy, M, N, torch.bfloat16, "dy")
+    _check_gscale(x_gscale)
+    _check_gscale(w_gscale)
+    dev = dy.device
+    dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev) if want_dx else None
+    dw = torch.empty((N, K), dtype=torch.bfloat16, device=dev) if want_dw else None
+    dbias = torch.empty(N, dtype=torch.float32, device=dev) if want_dbias else None
+    if workspace is None:
+        workspace = new_linear_backward_workspace(M, N, K, dev)
+    _check_workspace(workspace)
+    rc = lib.fp4attn_linear_backward(_ptr(dy), _row_stride(dy), _ptr(x_codes), _ptr(x_scales), _ptr(x_gscale),
+                                     _ptr(w_codes), _ptr(w_scales), _ptr(w_gscale), M, N, K, _ptr(dx), K, _ptr(dw),
+                                     _ptr(dbias), _ptr(workspace), workspace.numel(), _stream(None))
+    _check(rc, "fp4attn_linear_backward")
+    return dx, dw, dbias
+
+
+# -------------------------------------------- the norms around a branch --
+
+def _norm_vectors(C: int, post_weight, gate, pre_weight, scale, shift, groups: Optional[int]):
+    """(the C struct, number of samples) of the per-channel vectors."""
+    v = NormVectors()
+    for name, t in (("post_weight", post_weight), ("pre_weight", pre_weight)):
+        if t is not None:
+            assert t.shape == (C,) and t.dtype == torch.bfloat16 and t.stride(0) == 1, f"{name} is bf16 [{C}]"
+            _check_device(t)
+            setattr(v, name, t.data_ptr())
+    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
+        if t is not None:
+            t = t[None] if t.dim() == 1 else t
+            assert t.dim() == 2 and t.shape[1] == C and t.dtype == torch.bfloat16 and t.stride(1) == 1, \
+                f"{name} is bf16 [groups, {C}]"
+            assert groups is None or groups == t.shape[0], "gate, scale and shift share the number of samples"
+            groups = t.shape[0]
+            _check_device(t)
+            setattr(v, name, t.data_ptr())
+            setattr(v, name + "_stride", t.stride(0))
+    return v, 1 if groups is None else groups
+
+
+@_on_stream
+def fp4attn_norm_gate(x: torch.Tensor, h: Optional[torch.Tensor] = None, post_weight: Optional[torch.Tensor] = None,
+                      gate: Optional[torch.Tensor] = None, pre_weight: Optional[torch.Tensor] = None,
+                      scale: Optional[torch.Tensor] = None, shift: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                      flags: int = 0, groups: Optional[int] = None, want_y: bool = True, want_z: bool = True,
+                      quantize: bool = False, z_gscale: Optional[torch.Tensor] = None,
+                      y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> dict:
+    """y = x + gate * (post_weight * norm(h)) and z = norm(y) * pre_weight *
+    (1 + scale) + shift, on bf16 or fp32 rows x [rows, C] and bf16 h (None for
+    y = x).  RMS norms, or layer norms with flags=LAYER_NORM.  gate, scale and
+    shift are bf16 [groups, C], one row for each of `groups` equal samples.
+    quantize=True returns z as NVFP4 rows under the static scale z_gscale
+    (None for 1), ready for fp4attn_gemm.  y may be given (x itself for an
+    update in place).  Returns dict(y, z) or dict(y, z_codes, z_scales,
+    workspace)."""
+    rows, C = x.shape
+    dev = x.device
+    _check_rows(x, rows, C, x.dtype, "x")
+    if h is not None:
+        _check_rows(h, rows, C, torch.bfloat16, "h")
+    _check_gscale(z_gscale)
+    vec, G = _norm_vectors(C, post_weight, gate, pre_weight, scale, shift, groups)
+    if y is None and want_y:
+        y = torch.empty((rows, C), dtype=x.dtype, device=dev)
+    if y is not None:
+        _check_rows(y, rows, C, x.dtype, "y")
+    z = codes = scales = None
+    if quantize:
+        codes = torch.empty((rows, C // 2), dtype=torch.uint8, device=dev)
+        scales = torch.empty(fp4attn_scale_tile_bytes(rows, C), dtype=torch.uint8, device=dev)
+        if workspace is None:
+            workspace = new_linear_workspace(0, 0, 32, dev)
+    elif want_z:
+        z = torch.empty((rows, C), dtype=torch.bfloat16, device=dev)
+    if workspace is not None:
+        _check_workspace(workspace)
+    rc = lib.fp4attn_norm_gate(_ptr(x), _type_of(x), _row_stride(x), _ptr(h), 0 if h is None else _row_stride(h),
+                               ctypes.byref(vec), rows, C, G, float(eps), int(flags), _ptr(y),
+                               0 if y is None else _row_stride(y), _ptr(z), C, _ptr(codes), _ptr(scales),
+                               _ptr(z_gscale), _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                               _stream(None))
+    _check(rc, "fp4attn_norm_gate")
+    if quantize:
+        return dict(y=y, z_codes=codes, z_scales=scales, workspace=workspace)
+    return dict(y=y, z=z)
+
+
+@_on_stream
+def fp4attn_norm_gate_backward(dz: torch.Tensor, dy: Optional[torch.Tensor], y: torch.Tensor,
+                               h: Optional[torch.Tensor] = None, post_weight: Optional[torch.Tensor] = None,
+                               gate: Optional[torch.Tensor] = None, pre_weight: Optional[torch.Tensor] = None,
+                               scale: Optional[torch.Tensor] = None, eps: float = 1e-6, flags: int = 0,
+                               groups: Optional[int] = None, workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of fp4attn_norm_gate for bf16 dz and dy (y's type, None for 0)
+    from the forward's y and h: dict(dx, dh, dshift, dscale, dgate,
+    dpre_weight, dpost_weight); dh, dgate and dpost_weight are None without h.
+    Those of the vectors are fp32."""
+    rows, C = y.shape
+    dev = y.device
+    _check_rows(y, rows, C, y.dtype, "y")
+    _check_rows(dz, rows, C, torch.bfloat16, "dz")
+    if dy is not None:
+        _check_rows(dy, rows, C, y.dtype, "dy")
+    if h is not None:
+        _check_rows(h, rows, C, torch.bfloat16, "h")
+    vec, G = _norm_vectors(C, post_weight, gate, pre_weight, scale, None, groups)
+    if workspace is None:
+        workspace = new_norm_backward_workspace(rows, C, G, dev)
+    _check_workspace(workspace)
+    f32 = dict(dtype=torch.float32, device=dev)
+    out = dict(dx=torch.empty((rows, C), dtype=y.dtype, device=dev), dh=None, dshift=torch.empty((G, C), **f32),
+               dscale=torch.empty((G, C), **f32), dgate=None, dpre_weight=torch.empty(C, **f32), dpost_weight=None)
+    if h is not None:
+        out["dh"] = torch.empty((rows, C), dtype=torch.bfloat16, device=dev)
+        out["dgate"] = torch.empty((G, C), **f32)
+        out["dpost_weight"] = torch.empty(C, **f32)
+    rc = lib.fp4attn_norm_gate_backward(_ptr(dz), _row_stride(dz), _ptr(dy), 0 if dy is None else _row_stride(dy),
+                                        _ptr(y), _row_stride(y), _type_of(y), _ptr(h),
+                                        0 if h is None else _row_stride(h), ctypes.byref(vec), rows, C, G, float(eps),
+                                        int(flags), _ptr(out["dx"]), C, _ptr(out["dh"]), C, _ptr(out["dshift"]),
+                                        _ptr(out["dscale"]), _ptr(out["dgate"]), _ptr(out["dpre_weight"]),
+                                        _ptr(out["dpost_weight"]), _ptr(workspace), workspace.numel(), _stream(None))
+    _check(rc, "fp4attn_norm_gate_backward")
+    return out
 
 
 def fp4attn_read_status(workspace: torch.Tensor, stream=None) -> int:
