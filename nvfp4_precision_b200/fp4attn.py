@@ -414,11 +414,22 @@ def fp4_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, softmax_sca
 
 # ------------------------------------------------- linear layers in NVFP4 --
 
-def _check_device(t: torch.Tensor):
+# The calls below cost a few microseconds of host time each, next to kernels
+# that take as long for one row: they look up the device and the stream once
+# and pass addresses as plain integers.
+
+def _current_device() -> int:
+    return torch.cuda.current_device()
+
+
+def _wrong_device(t: torch.Tensor):
     """The library launches on the current device: a tensor of another one
     would be reached by address only, so it is refused."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensor on {t.device}: the library runs on the current CUDA device")
+    raise ValueError(f"tensor on {t.device}: the library runs on the current CUDA device")
+
+
+def _raw_stream(dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _on_stream(fn):
@@ -435,41 +446,57 @@ def _on_stream(fn):
     return call
 
 
-def _type_of(t: torch.Tensor) -> int:
-    assert t.dtype in (torch.bfloat16, torch.float32), "rows are bf16 or fp32"
-    return F32 if t.dtype == torch.float32 else BF16
+def _rows_of(t: torch.Tensor, dev: int, what: str, dtype: torch.dtype, rows: int, cols: int):
+    """(address, row stride) of a [rows, cols] matrix of contiguous rows."""
+    assert t.shape == (rows, cols) and t.dtype is dtype, f"{what} is {dtype} [{rows}, {cols}]"
+    if t.get_device() != dev:
+        _wrong_device(t)
+    assert cols <= 1 or t.stride(1) == 1, f"{what}: rows must be contiguous"
+    return t.data_ptr(), t.stride(0)
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    assert t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1), "rows must be contiguous"
-    return t.stride(0)
+def _type_of(dtype: torch.dtype) -> int:
+    assert dtype is torch.bfloat16 or dtype is torch.float32, "rows are bf16 or fp32"
+    return F32 if dtype is torch.float32 else BF16
 
 
-def _check_packed(codes: torch.Tensor, scales: torch.Tensor, what: str):
-    """(rows, K) of packed NVFP4 rows."""
-    assert codes.dtype == torch.uint8 and codes.dim() == 2 and codes.is_contiguous(), f"{what}: codes are uint8 [rows, K/2]"
-    rows, K = codes.shape[0], 2 * codes.shape[1]
-    assert scales.dtype == torch.uint8 and scales.is_contiguous() \
-        and scales.numel() == lib.fp4attn_scale_tile_bytes(rows, K), f"{what}: scale tiles of [{rows}, {K}]"
-    _check_device(codes)
-    _check_device(scales)
-    return rows, K
+def _packed_of(codes: torch.Tensor, scales: torch.Tensor, dev: int, what: str):
+    """(rows, K, address of the codes, address of the scales) of packed NVFP4 rows."""
+    assert codes.dtype is torch.uint8 and codes.dim() == 2 and codes.is_contiguous(), \
+        f"{what}: codes are uint8 [rows, K/2]"
+    rows, half = codes.shape
+    assert scales.dtype is torch.uint8 and scales.is_contiguous() \
+        and scales.numel() == (rows + 127) // 128 * ((half + 31) // 32) * 512, f"{what}: scale tiles of [{rows}, {2 * half}]"
+    if codes.get_device() != dev:
+        _wrong_device(codes)
+    if scales.get_device() != dev:
+        _wrong_device(scales)
+    return rows, 2 * half, codes.data_ptr(), scales.data_ptr()
 
 
-def _check_gscale(g: Optional[torch.Tensor]):
-    if g is not None:
-        assert g.dtype == torch.float32 and g.numel() == 1, "a scale is one fp32 on the device"
-        _check_device(g)
+def _gscale_of(g: Optional[torch.Tensor], dev: int):
+    if g is None:
+        return None
+    assert g.dtype is torch.float32 and g.numel() == 1, "a scale is one fp32 on the device"
+    if g.get_device() != dev:
+        _wrong_device(g)
+    return g.data_ptr()
 
 
-def _check_workspace(ws: torch.Tensor):
-    assert ws.dtype == torch.uint8 and ws.is_contiguous(), "a workspace is contiguous uint8"
-    _check_device(ws)
+def _vector_of(t: Optional[torch.Tensor], n: int, dev: int, what: str):
+    if t is None:
+        return None
+    assert t.shape == (n,) and t.dtype is torch.bfloat16 and (n <= 1 or t.stride(0) == 1), f"{what} is bf16 [{n}]"
+    if t.get_device() != dev:
+        _wrong_device(t)
+    return t.data_ptr()
 
 
-def _check_rows(t: torch.Tensor, rows: int, cols: int, dtype: torch.dtype, what: str):
-    assert t.shape == (rows, cols) and t.dtype == dtype, f"{what}: {dtype} [{rows}, {cols}]"
-    _check_device(t)
+def _workspace_of(ws: torch.Tensor, dev: int):
+    assert ws.dtype is torch.uint8 and ws.is_contiguous(), "a workspace is contiguous uint8"
+    if ws.get_device() != dev:
+        _wrong_device(ws)
+    return ws.data_ptr(), ws.numel()
 
 
 def fp4attn_scale_tile_bytes(rows: int, K: int) -> int:
@@ -526,23 +553,26 @@ def fp4attn_quantize_rows(x: torch.Tensor, gscale: Optional[torch.Tensor] = None
     stride that is a multiple of 8, or 4 for fp32).  dynamic_gscale=True
     computes the per-tensor scale into gscale (allocated when None) instead of
     reading it.  Returns dict(codes, scales, gscale, workspace)."""
-    _check_device(x)
-    _check_gscale(gscale)
+    dev = _current_device()
     rows, K = x.shape
-    dev = x.device
+    xt = _type_of(x.dtype)
+    xp, ld = _rows_of(x, dev, "x", x.dtype, rows, K)
     if codes is None:
-        codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=dev)
+        codes = x.new_empty((rows, K // 2), dtype=torch.uint8)
     if scales is None:
-        scales = torch.empty(fp4attn_scale_tile_bytes(rows, K), dtype=torch.uint8, device=dev)
-    assert _check_packed(codes, scales, "output") == (rows, K) or K % 32
+        scales = x.new_empty(fp4attn_scale_tile_bytes(rows, K // 32 * 32), dtype=torch.uint8)
+    if K % 32 == 0:
+        r, k, cp, sp = _packed_of(codes, scales, dev, "output")
+        assert r == rows and k == K, f"output: packed rows of [{rows}, {K}]"
+    else:
+        cp, sp = codes.data_ptr(), scales.data_ptr()  # refused below
     if workspace is None:
-        workspace = new_linear_workspace(0, 0, 32, dev)
-    _check_workspace(workspace)
+        workspace = new_linear_workspace(0, 0, 32, x.device)
+    ws, wsb = _workspace_of(workspace, dev)
     if dynamic_gscale and gscale is None:
-        gscale = torch.empty(1, dtype=torch.float32, device=dev)
-    rc = lib.fp4attn_quantize_rows(_ptr(x), _type_of(x), _row_stride(x), rows, K, _ptr(gscale),
-                                   DYNAMIC_GSCALE if dynamic_gscale else 0, _ptr(codes), _ptr(scales),
-                                   _ptr(workspace), workspace.numel(), _stream(None))
+        gscale = x.new_empty(1, dtype=torch.float32)
+    rc = lib.fp4attn_quantize_rows(xp, xt, ld, rows, K, _gscale_of(gscale, dev), DYNAMIC_GSCALE if dynamic_gscale else 0,
+                                   cp, sp, ws, wsb, _raw_stream(dev))
     _check(rc, "fp4attn_quantize_rows")
     return dict(codes=codes, scales=scales, gscale=gscale, workspace=workspace)
 
@@ -551,19 +581,13 @@ def fp4attn_quantize_rows(x: torch.Tensor, gscale: Optional[torch.Tensor] = None
 def fp4attn_dequant_rows(codes: torch.Tensor, scales: torch.Tensor, gscale: Optional[torch.Tensor] = None,
                          dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """The values of packed NVFP4 rows, bf16 or fp32 [rows, K]."""
-    rows, K = _check_packed(codes, scales, "rows")
-    _check_gscale(gscale)
-    out = torch.empty((rows, K), dtype=dtype, device=codes.device)
-    rc = lib.fp4attn_dequant_rows(_ptr(codes), _ptr(scales), _ptr(gscale), rows, K, _ptr(out), _type_of(out),
-                                  _stream(None))
+    dev = _current_device()
+    rows, K, cp, sp = _packed_of(codes, scales, dev, "rows")
+    out = codes.new_empty((rows, K), dtype=dtype)
+    rc = lib.fp4attn_dequant_rows(cp, sp, _gscale_of(gscale, dev), rows, K, out.data_ptr(), _type_of(dtype),
+                                  _raw_stream(dev))
     _check(rc, "fp4attn_dequant_rows")
     return out
-
-
-def _check_bias(bias: Optional[torch.Tensor], N: int):
-    if bias is not None:
-        assert bias.shape == (N,) and bias.dtype == torch.bfloat16 and bias.is_contiguous(), "bias is bf16 [N]"
-        _check_device(bias)
 
 
 @_on_stream
@@ -573,21 +597,18 @@ def fp4attn_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.T
                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y = g_x g_w x w^T + bias of packed NVFP4 x [M, K] and w [N, K]: bf16
     [M, N] (y may have any row stride)."""
-    M, K = _check_packed(x_codes, x_scales, "x")
-    N, K2 = _check_packed(w_codes, w_scales, "w")
+    dev = _current_device()
+    M, K, xc, xs = _packed_of(x_codes, x_scales, dev, "x")
+    N, K2, wc, wsc = _packed_of(w_codes, w_scales, dev, "w")
     assert K == K2, "x and w share K"
-    _check_gscale(x_gscale)
-    _check_gscale(w_gscale)
-    _check_bias(bias, N)
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x_codes.device)
-    _check_rows(y, M, N, torch.bfloat16, "y")
+        y = x_codes.new_empty((M, N), dtype=torch.bfloat16)
+    yp, ld = _rows_of(y, dev, "y", torch.bfloat16, M, N)
     if workspace is None:
         workspace = new_linear_workspace(0, 0, 32, x_codes.device)
-    _check_workspace(workspace)
-    rc = lib.fp4attn_gemm(_ptr(x_codes), _ptr(x_scales), _ptr(x_gscale), _ptr(w_codes), _ptr(w_scales),
-                          _ptr(w_gscale), _ptr(bias), M, N, K, _ptr(y), _row_stride(y), _ptr(workspace),
-                          workspace.numel(), _stream(None))
+    ws, wsb = _workspace_of(workspace, dev)
+    rc = lib.fp4attn_gemm(xc, xs, _gscale_of(x_gscale, dev), wc, wsc, _gscale_of(w_gscale, dev),
+                          _vector_of(bias, N, dev, "bias"), M, N, K, yp, ld, ws, wsb, _raw_stream(dev))
     _check(rc, "fp4attn_gemm")
     return y
 
@@ -600,23 +621,19 @@ def fp4attn_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tenso
     """The NVFP4 linear layer of bf16 x [M, K]: quantises x (per-tensor scale
     x_gscale, None for 1, or computed with dynamic_gscale) and multiplies by
     the packed weight [N, K].  bf16 [M, N]."""
-    assert x.dtype == torch.bfloat16, "x is bf16"
-    _check_device(x)
-    M, K = x.shape
-    N, K2 = _check_packed(w_codes, w_scales, "w")
-    assert K == K2, "x and w share K"
-    _check_gscale(x_gscale)
-    _check_gscale(w_gscale)
-    _check_bias(bias, N)
+    dev = _current_device()
+    N, K, wc, wsc = _packed_of(w_codes, w_scales, dev, "w")
+    M = x.shape[0]
+    xp, ldx = _rows_of(x, dev, "x", torch.bfloat16, M, K)
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    _check_rows(y, M, N, torch.bfloat16, "y")
+        y = x.new_empty((M, N))
+    yp, ld = _rows_of(y, dev, "y", torch.bfloat16, M, N)
     if workspace is None:
         workspace = new_linear_workspace(M, N, K, x.device)
-    _check_workspace(workspace)
-    rc = lib.fp4attn_linear(_ptr(x), _row_stride(x), _ptr(x_gscale), DYNAMIC_GSCALE if dynamic_gscale else 0,
-                            _ptr(w_codes), _ptr(w_scales), _ptr(w_gscale), _ptr(bias), M, N, K, _ptr(y),
-                            _row_stride(y), _ptr(workspace), workspace.numel(), _stream(None))
+    ws, wsb = _workspace_of(workspace, dev)
+    rc = lib.fp4attn_linear(xp, ldx, _gscale_of(x_gscale, dev), DYNAMIC_GSCALE if dynamic_gscale else 0, wc, wsc,
+                            _gscale_of(w_gscale, dev), _vector_of(bias, N, dev, "bias"), M, N, K, yp, ld, ws, wsb,
+                            _raw_stream(dev))
     _check(rc, "fp4attn_linear")
     return y
 
@@ -629,47 +646,44 @@ def fp4attn_linear_backward(dy: torch.Tensor, x_codes: torch.Tensor, x_scales: t
     """Straight-through gradients of fp4attn_linear for bf16 dy [M, N] and the
     packed operands of the forward: (dx bf16 [M, K], dw bf16 [N, K], dbias
     fp32 [N]), None in the place of one not wanted."""
-    M, K = _check_packed(x_codes, x_scales, "x")
-    N, K2 = _check_packed(w_codes, w_scales, "w")
+    dev = _current_device()
+    M, K, xc, xs = _packed_of(x_codes, x_scales, dev, "x")
+    N, K2, wc, wsc = _packed_of(w_codes, w_scales, dev, "w")
     assert K == K2, "x and w share K"
-    _check_rows(dy, M, N, torch.bfloat16, "dy")
-    _check_gscale(x_gscale)
-    _check_gscale(w_gscale)
-    dev = dy.device
-    dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev) if want_dx else None
-    dw = torch.empty((N, K), dtype=torch.bfloat16, device=dev) if want_dw else None
-    dbias = torch.empty(N, dtype=torch.float32, device=dev) if want_dbias else None
+    dyp, ld = _rows_of(dy, dev, "dy", torch.bfloat16, M, N)
+    dx = dy.new_empty((M, K)) if want_dx else None
+    dw = dy.new_empty((N, K)) if want_dw else None
+    dbias = dy.new_empty(N, dtype=torch.float32) if want_dbias else None
     if workspace is None:
-        workspace = new_linear_backward_workspace(M, N, K, dev)
-    _check_workspace(workspace)
-    rc = lib.fp4attn_linear_backward(_ptr(dy), _row_stride(dy), _ptr(x_codes), _ptr(x_scales), _ptr(x_gscale),
-                                     _ptr(w_codes), _ptr(w_scales), _ptr(w_gscale), M, N, K, _ptr(dx), K, _ptr(dw),
-                                     _ptr(dbias), _ptr(workspace), workspace.numel(), _stream(None))
+        workspace = new_linear_backward_workspace(M, N, K, dy.device)
+    ws, wsb = _workspace_of(workspace, dev)
+    rc = lib.fp4attn_linear_backward(dyp, ld, xc, xs, _gscale_of(x_gscale, dev), wc, wsc, _gscale_of(w_gscale, dev),
+                                     M, N, K, dx.data_ptr() if want_dx else None, K,
+                                     dw.data_ptr() if want_dw else None, dbias.data_ptr() if want_dbias else None,
+                                     ws, wsb, _raw_stream(dev))
     _check(rc, "fp4attn_linear_backward")
     return dx, dw, dbias
 
 
 # -------------------------------------------- the norms around a branch --
 
-def _norm_vectors(C: int, post_weight, gate, pre_weight, scale, shift, groups: Optional[int]):
+def _norm_vectors(C: int, dev: int, post_weight, gate, pre_weight, scale, shift, groups: Optional[int]):
     """(the C struct, number of samples) of the per-channel vectors."""
-    v = NormVectors()
-    for name, t in (("post_weight", post_weight), ("pre_weight", pre_weight)):
-        if t is not None:
-            assert t.shape == (C,) and t.dtype == torch.bfloat16 and t.stride(0) == 1, f"{name} is bf16 [{C}]"
-            _check_device(t)
-            setattr(v, name, t.data_ptr())
-    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
-        if t is not None:
-            t = t[None] if t.dim() == 1 else t
-            assert t.dim() == 2 and t.shape[1] == C and t.dtype == torch.bfloat16 and t.stride(1) == 1, \
-                f"{name} is bf16 [groups, {C}]"
-            assert groups is None or groups == t.shape[0], "gate, scale and shift share the number of samples"
-            groups = t.shape[0]
-            _check_device(t)
-            setattr(v, name, t.data_ptr())
-            setattr(v, name + "_stride", t.stride(0))
-    return v, 1 if groups is None else groups
+    v = [_vector_of(post_weight, C, dev, "post_weight"), _vector_of(pre_weight, C, dev, "pre_weight")]
+    for t in (gate, scale, shift):
+        if t is None:
+            v += (None, 0)
+            continue
+        shape = t.shape
+        G = shape[0] if len(shape) == 2 else 1
+        assert shape[-1] == C and len(shape) <= 2 and t.dtype is torch.bfloat16 and t.stride(-1) == 1, \
+            f"gate, scale and shift are bf16 [groups, {C}]"
+        assert groups is None or groups == G, "gate, scale and shift share the number of samples"
+        groups = G
+        if t.get_device() != dev:
+            _wrong_device(t)
+        v += (t.data_ptr(), t.stride(0) if len(shape) == 2 else C)
+    return NormVectors(*v), 1 if groups is None else groups
 
 
 @_on_stream
@@ -687,32 +701,32 @@ def fp4attn_norm_gate(x: torch.Tensor, h: Optional[torch.Tensor] = None, post_we
     (None for 1), ready for fp4attn_gemm.  y may be given (x itself for an
     update in place).  Returns dict(y, z) or dict(y, z_codes, z_scales,
     workspace)."""
+    dev = _current_device()
     rows, C = x.shape
-    dev = x.device
-    _check_rows(x, rows, C, x.dtype, "x")
-    if h is not None:
-        _check_rows(h, rows, C, torch.bfloat16, "h")
-    _check_gscale(z_gscale)
-    vec, G = _norm_vectors(C, post_weight, gate, pre_weight, scale, shift, groups)
+    dtype = x.dtype
+    xt = _type_of(dtype)
+    xp, ldx = _rows_of(x, dev, "x", dtype, rows, C)
+    hp, ldh = (None, 0) if h is None else _rows_of(h, dev, "h", torch.bfloat16, rows, C)
+    vec, G = _norm_vectors(C, dev, post_weight, gate, pre_weight, scale, shift, groups)
     if y is None and want_y:
-        y = torch.empty((rows, C), dtype=x.dtype, device=dev)
-    if y is not None:
-        _check_rows(y, rows, C, x.dtype, "y")
+        y = x.new_empty((rows, C))
+    yp, ldy = (None, 0) if y is None else _rows_of(y, dev, "y", dtype, rows, C)
     z = codes = scales = None
+    zp = cp = sp = gz = ws = None
+    wsb = 0
     if quantize:
-        codes = torch.empty((rows, C // 2), dtype=torch.uint8, device=dev)
-        scales = torch.empty(fp4attn_scale_tile_bytes(rows, C), dtype=torch.uint8, device=dev)
+        codes = x.new_empty((rows, C // 2), dtype=torch.uint8)
+        scales = x.new_empty(fp4attn_scale_tile_bytes(rows, C // 32 * 32), dtype=torch.uint8)
+        cp, sp, gz = codes.data_ptr(), scales.data_ptr(), _gscale_of(z_gscale, dev)
         if workspace is None:
-            workspace = new_linear_workspace(0, 0, 32, dev)
+            workspace = new_linear_workspace(0, 0, 32, x.device)
     elif want_z:
-        z = torch.empty((rows, C), dtype=torch.bfloat16, device=dev)
+        z = x.new_empty((rows, C), dtype=torch.bfloat16)
+        zp = z.data_ptr()
     if workspace is not None:
-        _check_workspace(workspace)
-    rc = lib.fp4attn_norm_gate(_ptr(x), _type_of(x), _row_stride(x), _ptr(h), 0 if h is None else _row_stride(h),
-                               ctypes.byref(vec), rows, C, G, float(eps), int(flags), _ptr(y),
-                               0 if y is None else _row_stride(y), _ptr(z), C, _ptr(codes), _ptr(scales),
-                               _ptr(z_gscale), _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                               _stream(None))
+        ws, wsb = _workspace_of(workspace, dev)
+    rc = lib.fp4attn_norm_gate(xp, xt, ldx, hp, ldh, vec, rows, C, G, eps, flags, yp, ldy, zp, C, cp, sp, gz, ws, wsb,
+                               _raw_stream(dev))
     _check(rc, "fp4attn_norm_gate")
     if quantize:
         return dict(y=y, z_codes=codes, z_scales=scales, workspace=workspace)
@@ -729,33 +743,34 @@ def fp4attn_norm_gate_backward(dz: torch.Tensor, dy: Optional[torch.Tensor], y: 
     from the forward's y and h: dict(dx, dh, dshift, dscale, dgate,
     dpre_weight, dpost_weight); dh, dgate and dpost_weight are None without h.
     Those of the vectors are fp32."""
+    dev = _current_device()
     rows, C = y.shape
-    dev = y.device
-    _check_rows(y, rows, C, y.dtype, "y")
-    _check_rows(dz, rows, C, torch.bfloat16, "dz")
-    if dy is not None:
-        _check_rows(dy, rows, C, y.dtype, "dy")
-    if h is not None:
-        _check_rows(h, rows, C, torch.bfloat16, "h")
-    vec, G = _norm_vectors(C, post_weight, gate, pre_weight, scale, None, groups)
+    dtype = y.dtype
+    yt = _type_of(dtype)
+    yp, ldy = _rows_of(y, dev, "y", dtype, rows, C)
+    dzp, lddz = _rows_of(dz, dev, "dz", torch.bfloat16, rows, C)
+    dyp, lddy = (None, 0) if dy is None else _rows_of(dy, dev, "dy", dtype, rows, C)
+    hp, ldh = (None, 0) if h is None else _rows_of(h, dev, "h", torch.bfloat16, rows, C)
+    vec, G = _norm_vectors(C, dev, post_weight, gate, pre_weight, scale, None, groups)
     if workspace is None:
-        workspace = new_norm_backward_workspace(rows, C, G, dev)
-    _check_workspace(workspace)
-    f32 = dict(dtype=torch.float32, device=dev)
-    out = dict(dx=torch.empty((rows, C), dtype=y.dtype, device=dev), dh=None, dshift=torch.empty((G, C), **f32),
-               dscale=torch.empty((G, C), **f32), dgate=None, dpre_weight=torch.empty(C, **f32), dpost_weight=None)
-    if h is not None:
-        out["dh"] = torch.empty((rows, C), dtype=torch.bfloat16, device=dev)
-        out["dgate"] = torch.empty((G, C), **f32)
-        out["dpost_weight"] = torch.empty(C, **f32)
-    rc = lib.fp4attn_norm_gate_backward(_ptr(dz), _row_stride(dz), _ptr(dy), 0 if dy is None else _row_stride(dy),
-                                        _ptr(y), _row_stride(y), _type_of(y), _ptr(h),
-                                        0 if h is None else _row_stride(h), ctypes.byref(vec), rows, C, G, float(eps),
-                                        int(flags), _ptr(out["dx"]), C, _ptr(out["dh"]), C, _ptr(out["dshift"]),
-                                        _ptr(out["dscale"]), _ptr(out["dgate"]), _ptr(out["dpre_weight"]),
-                                        _ptr(out["dpost_weight"]), _ptr(workspace), workspace.numel(), _stream(None))
+        workspace = new_norm_backward_workspace(rows, C, G, y.device)
+    ws, wsb = _workspace_of(workspace, dev)
+    dx = y.new_empty((rows, C))
+    dh = dgate = dpost = dhp = None
+    if h is None:
+        dshift, dscale = y.new_empty((2, G, C), dtype=torch.float32).unbind(0)
+        dpre = y.new_empty(C, dtype=torch.float32)
+    else:
+        dh = y.new_empty((rows, C), dtype=torch.bfloat16)
+        dhp = dh.data_ptr()
+        dshift, dscale, dgate = y.new_empty((3, G, C), dtype=torch.float32).unbind(0)
+        dpre, dpost = y.new_empty((2, C), dtype=torch.float32).unbind(0)
+    rc = lib.fp4attn_norm_gate_backward(dzp, lddz, dyp, lddy, yp, ldy, yt, hp, ldh, vec, rows, C, G, eps, flags,
+                                        dx.data_ptr(), C, dhp, C, dshift.data_ptr(), dscale.data_ptr(),
+                                        None if h is None else dgate.data_ptr(), dpre.data_ptr(),
+                                        None if h is None else dpost.data_ptr(), ws, wsb, _raw_stream(dev))
     _check(rc, "fp4attn_norm_gate_backward")
-    return out
+    return dict(dx=dx, dh=dh, dshift=dshift, dscale=dscale, dgate=dgate, dpre_weight=dpre, dpost_weight=dpost)
 
 
 def fp4attn_read_status(workspace: torch.Tensor, stream=None) -> int:
