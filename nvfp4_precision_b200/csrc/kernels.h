@@ -269,7 +269,6 @@ struct NormArgs {
     int C;
     float eps;
     bool layer;
-    bool pdl;           // let the launch behind this one start early
     void* y;            // may be nullptr
     int64_t ldy;
     __nv_bfloat16* z;   // may be nullptr
@@ -279,7 +278,8 @@ struct NormArgs {
     const float* gz;
     int64_t chunks;
     int* status;        // may be nullptr
-    int slots;          // set by the launcher
+    int cols;           // set by the launcher: channels per CTA, ring slots and their size
+    int slots;
     uint32_t slot_bytes;
 };
 int launch_norm_gate(const NormArgs& a, bool f32, cudaStream_t stream);
@@ -306,7 +306,8 @@ struct NormBwdArgs {
     float *dshift, *dscale, *dgate, *dpre, *dpost;  // [groups][C], [C]; each may be nullptr
     float* part;  // groups * parts * 3 * C
     int* status;
-    int slots;  // set by the launcher
+    int cols;  // set by the launcher
+    int slots;
     uint32_t slot_bytes;
 };
 int64_t norm_backward_parts(int64_t rows, int64_t C, int64_t groups);

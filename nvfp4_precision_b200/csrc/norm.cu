@@ -7,21 +7,29 @@
 //
 // (DiT blocks: Peebles and Xie, "Scalable Diffusion Models with Transformers",
 // 2023; a norm on the branch's output as well: Ding et al., "CogView", 2021.)
-// Both directions are bound by HBM: every row is read once and written once,
-// so what matters is that enough bytes are on their way at any time.
-//   * A team of threads holds one row in registers (statistics are sums over
-//     the team, fp32, in a fixed order) and walks down a contiguous range of
-//     rows.
+// Both directions are bound by HBM: every row is read once and written once.
+// What it takes to get there is few instructions per value and enough bytes on
+// their way at any time:
+//   * A team of threads holds a row in registers, up to 24 values a thread, and
+//     walks down a range of rows of one sample after another.  Products of the
+//     per-channel vectors (gate post_weight, pre_weight (1 + scale), shift) are
+//     made once per sample and stay in registers, as the backward's sums down
+//     the columns do; hence one CTA of 256 threads and 255 registers per SM.
+//     Rows wider than 256 * 24 channels are shared by a cluster.
 //   * The rows ahead come in by bulk copies into a ring in shared memory, one
-//     ring per team; a slot is filled again as soon as its row is in registers,
-//     so loads stay in flight through the reductions and the stores.
-//   * The per-channel vectors are read by every row and stay in L1.
+//     ring per team, so loads stay in flight through reductions and stores.
+//   * Two reductions over the team per row, for the layer norm too: its
+//     variance is taken about a pivot (the mean of eight values of the row)
+//     together with the mean, and again about that mean in the rare row whose
+//     pivot lay more than a standard deviation off, where the difference of
+//     squares would lose bits; y's mean follows from sums of the first pass.
 // The forward's z can leave as NVFP4 rows (rounded to bf16 first, as the
 // quantiser of a bf16 z would see it), so that the next linear layer reads
 // 9/16 byte a value instead of writing, reading and quantising 2-byte ones.
-// The backward's sums down the columns stay in registers over a team's rows;
-// the teams' parts meet in the workspace and are added in order: no atomics,
-// equal calls give equal bits.
+// The teams' column sums meet in the workspace and are added in order: no
+// atomics, equal calls give equal bits.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 
 #include "nvfp4_rows.cuh"
@@ -30,200 +38,346 @@ namespace fp4attn {
 
 namespace {
 
-constexpr int NTHREADS = 512;
+constexpr int NTHREADS = 256;
+constexpr int MAX_VALUES = 24;  // of a row, per thread
 constexpr uint64_t kLimitNs = 2000000000ull;  // 2 s: far beyond any legitimate wait
-constexpr int MAX_SLOTS = 4;
+constexpr uint64_t kDrainNs = 200000000ull;
+constexpr int MAX_SLOTS = 6;
+constexpr int MAX_CLUSTER = 4;
 
-template <int TPR>
-__device__ __forceinline__ void team_sync(int team) {
-    if constexpr (TPR == 32)
-        __syncwarp();
-    else
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(TPR) : "memory");
+// ---------------------------------------------------------------- teams --
+
+// A unit is what a thread loads at once: 8 values of bf16 rows, 4 of fp32 rows
+// (16 bytes of the residual either way, so that its stores fill whole sectors).
+template <int U>
+using Packed = std::conditional_t<U == 8, uint4, uint2>;
+
+__device__ __forceinline__ float2 pair_of(uint32_t w) { return make_float2(bf16lo(w), bf16hi(w)); }
+__device__ __forceinline__ void unpack(uint4 w, float2 (&v)[4]) {
+    v[0] = pair_of(w.x), v[1] = pair_of(w.y), v[2] = pair_of(w.z), v[3] = pair_of(w.w);
+}
+__device__ __forceinline__ void unpack(uint2 w, float2 (&v)[2]) { v[0] = pair_of(w.x), v[1] = pair_of(w.y); }
+__device__ __forceinline__ uint32_t pack_pair(float2 v) { return pack_bf16x2(v.x, v.y); }
+__device__ __forceinline__ uint4 pack(const float2 (&v)[4]) {
+    return make_uint4(pack_pair(v[0]), pack_pair(v[1]), pack_pair(v[2]), pack_pair(v[3]));
+}
+__device__ __forceinline__ uint2 pack(const float2 (&v)[2]) { return make_uint2(pack_pair(v[0]), pack_pair(v[1])); }
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+// Residual units in shared or global memory.
+__device__ __forceinline__ void load_res(const void* row, int u, float2 (&v)[4]) {
+    unpack(static_cast<const uint4*>(row)[u], v);
+}
+__device__ __forceinline__ void load_res(const void* row, int u, float2 (&v)[2]) {
+    const float4 f = static_cast<const float4*>(row)[u];
+    v[0] = make_float2(f.x, f.y), v[1] = make_float2(f.z, f.w);
+}
+__device__ __forceinline__ void store_res(void* row, int u, const float2 (&v)[4]) { static_cast<uint4*>(row)[u] = pack(v); }
+__device__ __forceinline__ void store_res(void* row, int u, const float2 (&v)[2]) {
+    static_cast<float4*>(row)[u] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+}
+template <int U>
+__device__ __forceinline__ float res_value(const void* row, int i) {
+    if constexpr (U == 8) return __bfloat162float(static_cast<const __nv_bfloat16*>(row)[i]);
+    return static_cast<const float*>(row)[i];
 }
 
-// Sums over the team of K values per thread, the same bits in every thread.
-// `scratch` holds two buffers that alternate, so one barrier per sum is enough.
-template <int TPR, int K>
-__device__ __forceinline__ void team_sum(float (&v)[K], float* scratch, int& phase, int team) {
-    constexpr int W = TPR / 32;
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-    if constexpr (W == 1) {
-        __syncwarp();
+// The values of a unit of a bf16 vector, or `absent` for a null one.
+template <int U>
+__device__ __forceinline__ void load_vector(const __nv_bfloat16* p, int64_t at, float absent, float2 (&v)[U / 2]) {
+    if (p) {
+        unpack(__ldg(reinterpret_cast<const Packed<U>*>(p + at)), v);
     } else {
-        float* at = scratch + phase * (4 * W);
-        phase ^= 1;
-        const int warp = (threadIdx.x % TPR) >> 5;
-        if ((threadIdx.x & 31) == 0)
 #pragma unroll
-            for (int k = 0; k < K; ++k) at[k * W + warp] = v[k];
-        team_sync<TPR>(team);
+        for (int i = 0; i < U / 2; ++i) v[i] = both(absent);
+    }
+}
+
+// What a thread knows of its team: TPR threads of the CTA, or (WIDE) the CTAs
+// of the cluster together.
+template <int TPR, bool WIDE>
+struct Team {
+    static constexpr int W = TPR / 32;
+    static constexpr int MAX_PARTS = W * (WIDE ? MAX_CLUSTER : 1);
+    static constexpr int MAX_K = 6;
+    static constexpr int SCRATCH = 2 * MAX_K * MAX_PARTS;  // floats per team: two buffers that alternate
+    float* scratch;
+    int index, phase;
+    uint32_t rank, ranks;
+
+    __device__ __forceinline__ void sync() const {
+        if constexpr (WIDE)
+            cluster_sync();
+        else if constexpr (TPR == 32)
+            __syncwarp();
+        else
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + index), "n"(TPR) : "memory");
+    }
+
+    // Sums over the team of K values a thread, the same bits in every thread.
+    // Ends every use that the threads made of shared memory before it.
+    template <int K>
+    __device__ __forceinline__ void sum(float (&v)[K]) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            float s = 0.0f;
+        for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-            for (int w = 0; w < W; ++w) s += at[k * W + w];
-            v[k] = s;
+            for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+        if constexpr (W == 1 && !WIDE) {
+            __syncwarp();
+        } else {
+            float* at = scratch + phase * (MAX_K * MAX_PARTS);
+            phase ^= 1;
+            const int warp = (threadIdx.x % TPR) >> 5, lane = threadIdx.x & 31;
+            if constexpr (WIDE) {
+                if (lane < (int)ranks) {
+                    const uint32_t base = mapa(smem_u32(at), (uint32_t)lane);
+#pragma unroll
+                    for (int k = 0; k < K; ++k) st_cluster(base + 4u * (k * MAX_PARTS + rank * W + warp), v[k]);
+                }
+            } else if (lane == 0) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) at[k * MAX_PARTS + warp] = v[k];
+            }
+            sync();
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float s = 0.0f;
+                if constexpr (WIDE) {
+                    for (int w = 0; w < (int)ranks * W; ++w) s += at[k * MAX_PARTS + w];
+                } else {
+#pragma unroll
+                    for (int w = 0; w < W; ++w) s += at[k * MAX_PARTS + w];
+                }
+                v[k] = s;
+            }
         }
     }
-}
+};
 
-__device__ __forceinline__ void unpack8(uint4 w, float (&v)[8]) {
-    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+// The columns of a CTA: all of them, or a share of whole 64-channel chunks.
+__device__ __forceinline__ int first_column(int cols_per_cta, uint32_t rank) { return cols_per_cta * (int)rank; }
+
+// Mean of eight values spread over the row (of this CTA's columns).
+template <int U>
+__device__ __forceinline__ float pivot_of(const void* row, int cols) {
+    float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16lo(x[i]);
-        v[2 * i + 1] = bf16hi(x[i]);
+    for (int i = 0; i < 8; ++i) s += res_value<U>(row, (int)((unsigned)cols * (unsigned)i / 8u));
+    return 0.125f * s;
+}
+// The same pivot for every CTA of a cluster.
+template <int TPR, bool WIDE>
+__device__ __forceinline__ void share_pivots(Team<TPR, WIDE>& team, float& p, float& q) {
+    if constexpr (WIDE) {
+        float v[2] = {threadIdx.x == 0 ? p : 0.0f, threadIdx.x == 0 ? q : 0.0f};
+        team.sum(v);
+        p = v[0] / (float)team.ranks;
+        q = v[1] / (float)team.ranks;
     }
 }
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-}
-__device__ __forceinline__ void unpack4(uint2 w, float (&v)[4]) {
-    v[0] = bf16lo(w.x);
-    v[1] = bf16hi(w.x);
-    v[2] = bf16lo(w.y);
-    v[3] = bf16hi(w.y);
-}
-__device__ __forceinline__ uint4 ldg16(const __nv_bfloat16* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
-__device__ __forceinline__ uint2 ldg8(const __nv_bfloat16* p) { return __ldg(reinterpret_cast<const uint2*>(p)); }
-constexpr uint32_t kOnes = 0x3F803F80u;  // two bf16 ones
-__device__ __forceinline__ uint4 ldg16_or(const __nv_bfloat16* p, int64_t at, uint32_t w) {
-    return p ? ldg16(p + at) : make_uint4(w, w, w, w);
-}
-__device__ __forceinline__ uint2 ldg8_or(const __nv_bfloat16* p, int64_t at, uint32_t w) {
-    return p ? ldg8(p + at) : make_uint2(w, w);
-}
-
-// One team's ring: `slots` rows on their way or in use.  Thread 0 of the team
-// fills a slot once every thread has its row in registers.
-struct Ring {
-    uint8_t* buf;
-    uint32_t bars;   // shared address of the slots' barriers
-    uint32_t slot_bytes;
-    int slots;
-};
 
 // ------------------------------------------------------------- forward --
 
-template <int TPR, int J, bool F32, bool QUANT>
-__global__ void __launch_bounds__(NTHREADS) norm_gate_kernel(const __grid_constant__ NormArgs a) {
-    constexpr int TEAMS = NTHREADS / TPR, ES = F32 ? 4 : 2;
+template <int TPR, int J, int U, bool LAYER, bool QUANT, bool WIDE>
+__global__ void __launch_bounds__(NTHREADS, 1) norm_gate_kernel(const __grid_constant__ NormArgs a) {
+    constexpr int TEAMS = NTHREADS / TPR, ES = U == 4 ? 4 : 2, P = U / 2;
+    using TeamT = Team<TPR, WIDE>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t bars[TEAMS * MAX_SLOTS];
-    __shared__ __align__(16) float scratch_all[TEAMS * 8 * (TPR / 32)];
+    __shared__ __align__(16) float scratch[TEAMS * TeamT::SCRATCH];
     __shared__ int abort_all;
-    const int team = threadIdx.x / TPR, t = threadIdx.x % TPR;
-    const int C = a.C, NV = C / 8;
-    float* scratch = scratch_all + team * 8 * (TPR / 32);
+    const int t = threadIdx.x % TPR;
+    TeamT team;
+    team.index = threadIdx.x / TPR;
+    team.scratch = scratch + team.index * TeamT::SCRATCH;
+    team.phase = 0;
+    team.rank = WIDE ? cluster_ctarank() : 0;
+    team.ranks = WIDE ? cluster_nctarank() : 1;
+    const int c0 = first_column(a.cols, team.rank), cols = min(a.cols, a.C - c0), NU = cols / U;
     if (threadIdx.x == 0) abort_all = 0;
     if (threadIdx.x < TEAMS * MAX_SLOTS) mbar_init(smem_u32(&bars[threadIdx.x]), 1);
     fence_mbar_init();
     __syncthreads();
-    if (a.pdl) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if constexpr (WIDE) cluster_sync();
     volatile int* abort_flag = &abort_all;
 
     const bool has_h = a.h != nullptr;
-    const uint32_t x_bytes = (uint32_t)C * ES, h_bytes = has_h ? (uint32_t)C * 2 : 0;
-    uint8_t* ring = smem + (size_t)team * a.slots * a.slot_bytes;
-    const uint32_t ring_u = smem_u32(ring);
-    const int64_t team_id = blockIdx.x + (int64_t)gridDim.x * team, n_teams = (int64_t)gridDim.x * TEAMS;
-    const int64_t r0 = a.rows * team_id / n_teams, r1 = a.rows * (team_id + 1) / n_teams;
-    auto fill = [&](int64_t row, int slot) {
-        const uint32_t bar = smem_u32(&bars[team * MAX_SLOTS + slot]);
-        const uint32_t at = ring_u + a.slot_bytes * slot;
+    const uint32_t x_bytes = (uint32_t)cols * ES, h_bytes = has_h ? (uint32_t)cols * 2 : 0;
+    const uint8_t* ring = smem + (size_t)team.index * a.slots * a.slot_bytes;
+    const uint32_t ring_u = smem_u32(ring), bars_u = smem_u32(&bars[team.index * MAX_SLOTS]);
+    const int64_t teams = (int64_t)(gridDim.x / team.ranks) * TEAMS;
+    const int64_t id = blockIdx.x / team.ranks + (int64_t)(gridDim.x / team.ranks) * team.index;
+    const int64_t r0 = a.rows * id / teams, r1 = a.rows * (id + 1) / teams;
+    const uint8_t* x_at = static_cast<const uint8_t*>(a.x) + (r0 * a.ldx + c0) * ES;
+    const __nv_bfloat16* h_at = a.h + (r0 * a.ldh + c0);
+    auto fill = [&](int slot) {  // of the next row, by thread 0
+        const uint32_t bar = bars_u + 8u * slot, at = ring_u + a.slot_bytes * slot;
         mbar_arrive_expect_tx(bar, x_bytes + h_bytes);
-        bulk_load(at, static_cast<const uint8_t*>(a.x) + row * a.ldx * ES, x_bytes, bar);
-        if (has_h) bulk_load(at + x_bytes, a.h + row * a.ldh, h_bytes, bar);
+        bulk_load(at, x_at, x_bytes, bar);
+        x_at += a.ldx * ES;
+        if (has_h) {
+            bulk_load(at + x_bytes, h_at, h_bytes, bar);
+            h_at += a.ldh;
+        }
     };
     int64_t next = r0;
     if (t == 0)
-        for (int s = 0; s < a.slots && next < r1; ++s, ++next) fill(next, s);
+        for (int s = 0; s < a.slots && next < r1; ++s, ++next) fill(s);
     const float gz = QUANT ? (a.gz ? __ldg(a.gz) : 1.0f) : 1.0f;
     if (QUANT && blockIdx.x == 0 && threadIdx.x == 0 && bad_gscale(gz)) raise_status(a.status, FP4ATTN_ERR_RANGE);
-    const float inv_c = 1.0f / (float)C;
-    bool finite = true;
-    int phase = 0, slot = 0;
-    uint32_t parity = 0;
+    const float inv_c = 1.0f / (float)a.C;
+
+    // gate post_weight, pre_weight (1 + scale) and shift of this thread's channels
+    float2 A[J][P], B[J][P], S[J][P];
+    float mean_A = 0.0f;
     int64_t group = r0 < r1 ? r0 / a.rows_per_group : 0;
-    int64_t group_end = (group + 1) * a.rows_per_group;
-    for (int64_t row = r0; row < r1; ++row) {
+    int64_t group_end = group * a.rows_per_group;  // none loaded yet
+
+    bool finite = true;
+    int slot = 0;
+    uint32_t parity = 0;
+    uint8_t* y_at = static_cast<uint8_t*>(a.y) + (r0 * a.ldy + c0) * ES;
+    __nv_bfloat16* z_at = a.z + (r0 * a.ldz + c0);
+    for (int64_t row = r0; row < r1; ++row, y_at += a.ldy * ES, z_at += a.ldz) {
         if (row >= group_end) {
-            ++group;
+            if (row > r0) ++group;
             group_end += a.rows_per_group;
+            if (row == r0) group_end = (group + 1) * a.rows_per_group;
+            float s[1] = {0.0f};
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int u = t + TPR * j;
+                const bool on = u < NU;
+                const int64_t c = on ? c0 + U * u : 0;
+                float2 p[P], q[P];
+                load_vector<U>(a.gate, group * a.lgate + c, 1.0f, p);
+                load_vector<U>(a.post, c, 1.0f, q);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    A[j][i] = on ? __fmul2_rn(p[i], q[i]) : both(0.0f);
+                    s[0] += A[j][i].x + A[j][i].y;
+                }
+                load_vector<U>(a.pre, c, 1.0f, p);
+                load_vector<U>(a.scale, group * a.lscale + c, 0.0f, q);
+#pragma unroll
+                for (int i = 0; i < P; ++i) B[j][i] = on ? __ffma2_rn(p[i], q[i], p[i]) : both(0.0f);
+                load_vector<U>(a.shift, group * a.lshift + c, 0.0f, p);
+#pragma unroll
+                for (int i = 0; i < P; ++i) S[j][i] = on ? p[i] : both(0.0f);
+            }
+            if (LAYER) {
+                team.sum(s);
+                mean_A = s[0] * inv_c;
+            }
         }
-        const bool ok = mbar_wait(smem_u32(&bars[team * MAX_SLOTS + slot]), parity, abort_flag, a.status, kLimitNs);
+        const bool ok = mbar_wait(bars_u + 8u * slot, parity, abort_flag, a.status, kLimitNs);
         const uint8_t* at = ring + (size_t)a.slot_bytes * slot;
-        float yv[J][8];
-        uint4 hv[J], pv[J], gv[J];
+        float2 y[J][P];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const int v = t + TPR * j;
-            if (v < NV) {
-                if constexpr (F32) {
-                    const float4 lo = reinterpret_cast<const float4*>(at)[2 * v];
-                    const float4 hi = reinterpret_cast<const float4*>(at)[2 * v + 1];
-                    const float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) yv[j][i] = f[i];
-                } else {
-                    unpack8(reinterpret_cast<const uint4*>(at)[v], yv[j]);
-                }
-                if (has_h) {
-                    hv[j] = reinterpret_cast<const uint4*>(at + x_bytes)[v];
-                    pv[j] = ldg16_or(a.post, 8 * v, kOnes);
-                    gv[j] = ldg16_or(a.gate, group * a.lgate + 8 * v, kOnes);
-                }
+            const int u = t + TPR * j;
+            if (u < NU) {
+                load_res(at, u, y[j]);
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) yv[j][i] = 0.0f;
-                hv[j] = pv[j] = gv[j] = make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < P; ++i) y[j][i] = both(0.0f);
             }
             // a row that never came (its wait ran out) must not pass for one
-            if (!ok)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) yv[j][i] = __int_as_float(0x7FC00000);
+            if (!ok) y[j][0].x = __int_as_float(0x7FC00000);
         }
-        if (!has_h) team_sync<TPR>(team);
+        float mean = 0.0f;  // of y: where its sums are taken about
         if (has_h) {
-            float mean = 0.0f, q[1] = {0.0f};
-            if (a.layer) {
-                float s[1] = {0.0f};
+            Packed<U> h[J];
+            float q = 0.0f, unused = 0.0f;
+            if (LAYER) {
+                q = pivot_of<8>(at + x_bytes, cols);
+                share_pivots(team, q, unused);
+            }
+            // channels past the row's end hold the pivot and add nothing
+            const uint32_t fill_w = pack_bf16x2(q, q);
+            if (LAYER) q = bf16lo(fill_w);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int u = t + TPR * j;
+                if (u < NU) {
+                    h[j] = reinterpret_cast<const Packed<U>*>(at + x_bytes)[u];
+                } else {
+                    if constexpr (U == 8)
+                        h[j] = make_uint4(fill_w, fill_w, fill_w, fill_w);
+                    else
+                        h[j] = make_uint2(fill_w, fill_w);
+                }
+            }
+            float r, mean_h = 0.0f;
+            if constexpr (!LAYER) {
+                float2 s2 = both(0.0f);
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
-                    float f[8];
-                    unpack8(hv[j], f);
+                    float2 f[P];
+                    unpack(h[j], f);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) s[0] += f[i];
+                    for (int i = 0; i < P; ++i) s2 = __ffma2_rn(f[i], f[i], s2);
                 }
-                team_sum<TPR, 1>(s, scratch, phase, team);
-                mean = s[0] * inv_c;
+                float s[1] = {s2.x + s2.y};
+                team.sum(s);
+                r = rsqrtf(__fmaf_rn(s[0], inv_c, a.eps));
+            } else {
+                float off = q;
+                for (int again = 0;; ++again) {
+                    // sums about the pivot; those of x and A (h - pivot) lead to y's mean
+                    float2 s1 = both(0.0f), s2 = both(0.0f), sx = both(0.0f), sa = both(0.0f);
+                    const float2 o2 = both(-off);
+#pragma unroll
+                    for (int j = 0; j < J; ++j) {
+                        float2 f[P];
+                        unpack(h[j], f);
+#pragma unroll
+                        for (int i = 0; i < P; ++i) {
+                            f[i] = __fadd2_rn(f[i], o2);
+                            if (again && t + TPR * j >= NU) f[i] = both(0.0f);
+                            s1 = __fadd2_rn(s1, f[i]);
+                            s2 = __ffma2_rn(f[i], f[i], s2);
+                            sa = __ffma2_rn(f[i], A[j][i], sa);
+                            sx = __fadd2_rn(sx, y[j][i]);
+                        }
+                    }
+                    float s[4] = {s1.x + s1.y, s2.x + s2.y, sa.x + sa.y, sx.x + sx.y};
+                    team.sum(s);
+                    const float d = s[0] * inv_c, var = __fmaf_rn(-d, d, s[1] * inv_c);
+                    mean_h = off + d;
+                    r = rsqrtf(fmaxf(var, 0.0f) + a.eps);
+                    mean = s[3] * inv_c + r * (s[2] * inv_c - d * mean_A);
+                    if (again || d * d <= var) break;
+                    off = mean_h;
+                }
             }
+            const float2 m2 = both(-mean_h), r2 = both(r);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                float f[8];
-                unpack8(hv[j], f);
-                if (t + TPR * j < NV)
+                float2 f[P];
+                unpack(h[j], f);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) q[0] = __fmaf_rn(f[i] - mean, f[i] - mean, q[0]);
+                for (int i = 0; i < P; ++i) {
+                    if (LAYER) f[i] = __fadd2_rn(f[i], m2);
+                    y[j][i] = __ffma2_rn(A[j][i], __fmul2_rn(f[i], r2), y[j][i]);
+                }
             }
-            team_sum<TPR, 1>(q, scratch, phase, team);
-            const float r = rsqrtf(__fmaf_rn(q[0], inv_c, a.eps));
+        } else if (LAYER) {
+            float s[1] = {0.0f};
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                float f[8], p[8], g[8];
-                unpack8(hv[j], f);
-                unpack8(pv[j], p);
-                unpack8(gv[j], g);
+            for (int j = 0; j < J; ++j)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) yv[j][i] = __fmaf_rn(g[i] * p[i], (f[i] - mean) * r, yv[j][i]);
-            }
+                for (int i = 0; i < P; ++i) s[0] += y[j][i].x + y[j][i].y;
+            team.sum(s);
+            mean = s[0] * inv_c;
+        } else {
+            team.sync();
         }
-        // every thread has passed a barrier behind its loads: the slot is free
-        if (t == 0 && next < r1 && !*abort_flag) fill(next++, slot);
+        // every thread has its row: the slot is free
+        if (t == 0 && next < r1 && !*abort_flag) {
+            fill(slot);
+            ++next;
+        }
         if (++slot == a.slots) {
             slot = 0;
             parity ^= 1;
@@ -231,80 +385,76 @@ __global__ void __launch_bounds__(NTHREADS) norm_gate_kernel(const __grid_consta
         if (a.y) {
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                const int v = t + TPR * j;
-                if (v < NV && FP4ATTN_IN_BOUNDS(row < a.rows && 8 * v + 8 <= C, a.status)) {
-                    if constexpr (F32) {
-                        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.y) + row * a.ldy + 8 * v);
-                        dst[0] = make_float4(yv[j][0], yv[j][1], yv[j][2], yv[j][3]);
-                        dst[1] = make_float4(yv[j][4], yv[j][5], yv[j][6], yv[j][7]);
-                    } else {
-                        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y) + row * a.ldy + 8 * v) = pack8(yv[j]);
-                    }
-                }
+                const int u = t + TPR * j;
+                if (u < NU && FP4ATTN_IN_BOUNDS(row < a.rows && c0 + U * u + U <= a.C, a.status)) store_res(y_at, u, y[j]);
             }
         }
         if (!QUANT && !a.z) continue;
-        uint4 sc[J], sh[J];
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int v = t + TPR * j;
-            pv[j] = sc[j] = sh[j] = make_uint4(0, 0, 0, 0);
-            if (v < NV) {
-                pv[j] = ldg16_or(a.pre, 8 * v, kOnes);
-                sc[j] = ldg16_or(a.scale, group * a.lscale + 8 * v, 0u);
-                sh[j] = ldg16_or(a.shift, group * a.lshift + 8 * v, 0u);
-            }
-        }
-        float mean = 0.0f, q[1] = {0.0f};
-        if (a.layer) {
-            float s[1] = {0.0f};
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-                if (t + TPR * j < NV)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) s[0] += yv[j][i];
-            team_sum<TPR, 1>(s, scratch, phase, team);
-            mean = s[0] * inv_c;
-        }
+        float2 s1 = both(0.0f), s2 = both(0.0f);
 #pragma unroll
         for (int j = 0; j < J; ++j)
-            if (t + TPR * j < NV)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) q[0] = __fmaf_rn(yv[j][i] - mean, yv[j][i] - mean, q[0]);
-        team_sum<TPR, 1>(q, scratch, phase, team);
-        const float r = rsqrtf(__fmaf_rn(q[0], inv_c, a.eps));
+            for (int i = 0; i < P; ++i) {
+                if constexpr (LAYER) {
+                    y[j][i] = t + TPR * j < NU ? __fadd2_rn(y[j][i], both(-mean)) : both(0.0f);
+                    s1 = __fadd2_rn(s1, y[j][i]);
+                }
+                s2 = __ffma2_rn(y[j][i], y[j][i], s2);
+            }
+        float d = 0.0f, r;
+        if constexpr (LAYER) {
+            float s[2] = {s1.x + s1.y, s2.x + s2.y};
+            team.sum(s);
+            d = s[0] * inv_c;
+            r = rsqrtf(fmaxf(__fmaf_rn(-d, d, s[1] * inv_c), 0.0f) + a.eps);
+        } else {
+            float s[1] = {s2.x + s2.y};
+            team.sum(s);
+            r = rsqrtf(__fmaf_rn(s[0], inv_c, a.eps));
+        }
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const int v = t + TPR * j;
-            float p[8], s[8], b[8], z[8];
-            unpack8(pv[j], p);
-            unpack8(sc[j], s);
-            unpack8(sh[j], b);
+            const int u = t + TPR * j;
+            float2 z[P];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = __fmaf_rn((yv[j][i] - mean) * r, __fmaf_rn(p[i], s[i], p[i]), b[i]);
-            const uint4 w = pack8(z);
+            for (int i = 0; i < P; ++i) {
+                const float2 n = LAYER ? __fadd2_rn(y[j][i], both(-d)) : y[j][i];
+                z[i] = __ffma2_rn(__fmul2_rn(n, both(r)), B[j][i], S[j][i]);
+            }
+            const Packed<U> w = pack(z);
             if constexpr (!QUANT) {
-                if (v < NV && FP4ATTN_IN_BOUNDS(row < a.rows && 8 * v + 8 <= C, a.status))
-                    *reinterpret_cast<uint4*>(a.z + row * a.ldz + 8 * v) = w;
+                if (u < NU && FP4ATTN_IN_BOUNDS(row < a.rows && c0 + U * u + U <= a.C, a.status))
+                    reinterpret_cast<Packed<U>*>(z_at)[u] = w;
             } else {
-                // two lanes share a block of 16 values, eight a word of four scales
-                unpack8(w, z);
+                // 16 / U lanes share a block, 64 / U a word of four scales
+                unpack(w, z);
                 float m = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(z[i]));
-                if (v >= NV) m = 0.0f;
-                m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                for (int i = 0; i < P; ++i) m = max_nan(m, max_nan(fabsf(z[i].x), fabsf(z[i].y)));
+                if (u >= NU) m = 0.0f;
+#pragma unroll
+                for (int o = 1; o < 16 / U; o *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
                 finite = finite && (m < INFINITY);
                 uint32_t s8;
                 float inv;
                 row_block_scale(m, gz, s8, inv);
-                if (v < NV && FP4ATTN_IN_BOUNDS(row < a.rows && 8 * v + 8 <= C, a.status))
-                    *reinterpret_cast<uint32_t*>(a.codes + row * (C / 2) + 4 * v) = row_codes8(z, inv);
-                uint32_t word = s8 << (8 * ((v >> 1) & 3));
-                word |= __shfl_xor_sync(0xffffffffu, word, 2);
-                word |= __shfl_xor_sync(0xffffffffu, word, 4);
-                const int64_t off = ((row >> 7) * a.chunks + (v >> 3)) * 128 + scale_word_in_tile((uint32_t)row & 127);
-                if ((v & 7) == 0 && v < NV && FP4ATTN_IN_BOUNDS(4 * off + 4 <= scale_tile_bytes(a.rows, C), a.status))
+#pragma unroll
+                for (int i = 0; i < P; ++i) z[i] = __fmul2_rn(z[i], both(inv));
+                const bool on = u < NU && FP4ATTN_IN_BOUNDS(row < a.rows && c0 + U * u + U <= a.C, a.status);
+                uint8_t* codes = a.codes + row * (a.C / 2) + (c0 + U * u) / 2;
+                if constexpr (U == 8) {
+                    const uint32_t c = cvt_e2m1x8(z[0].x, z[0].y, z[1].x, z[1].y, z[2].x, z[2].y, z[3].x, z[3].y);
+                    if (on) *reinterpret_cast<uint32_t*>(codes) = c;
+                } else {
+                    const uint32_t c = cvt_e2m1x8(z[0].x, z[0].y, z[1].x, z[1].y, 0.0f, 0.0f, 0.0f, 0.0f);
+                    if (on) *reinterpret_cast<uint16_t*>(codes) = (uint16_t)c;
+                }
+                uint32_t word = s8 << (8 * ((u * U / 16) & 3));
+#pragma unroll
+                for (int o = 16 / U; o < 64 / U; o *= 2) word |= __shfl_xor_sync(0xffffffffu, word, o);
+                const int64_t off =
+                    ((row >> 7) * a.chunks + (c0 + U * u) / 64) * 128 + scale_word_in_tile((uint32_t)row & 127);
+                if (on && u % (64 / U) == 0 && FP4ATTN_IN_BOUNDS(4 * off + 4 <= scale_tile_bytes(a.rows, a.C), a.status))
                     reinterpret_cast<uint32_t*>(a.scales)[off] = word;
             }
         }
@@ -314,7 +464,7 @@ __global__ void __launch_bounds__(NTHREADS) norm_gate_kernel(const __grid_consta
         // this team's own copies land before it leaves (bounded)
         int dummy = 0;
         for (int s = 0; s < a.slots; ++s)
-            for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait(smem_u32(&bars[team * MAX_SLOTS + s]), ph, &dummy, nullptr, 200000000ull);
+            for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait(bars_u + 8u * s, ph, &dummy, nullptr, kDrainNs);
     }
 }
 
@@ -324,234 +474,263 @@ __global__ void __launch_bounds__(NTHREADS) norm_gate_kernel(const __grid_consta
 //   dx = dy + r (dn - n mean(dn n) - [layer] mean(dn))
 // and with m = norm(h), dm = dx gate post:
 //   dh = r_h (dm - m mean(dm m) - [layer] mean(dm))
-// Sums down the rows of a sample: dz, dz n, dx m.
+// Sums down the rows of a sample: dz, dz n, dx m.  A row is read from its slot
+// twice (y and dy need not stay in registers in between); the slot is filled
+// again one row later, behind the barrier that shows that everyone is done.
 
-template <int TPR, int J, bool F32>
-__global__ void __launch_bounds__(NTHREADS) norm_gate_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
-    constexpr int TEAMS = NTHREADS / TPR, ES = F32 ? 4 : 2;
+template <int TPR, int J, int U, bool LAYER, bool WIDE>
+__global__ void __launch_bounds__(NTHREADS, 1) norm_gate_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
+    constexpr int TEAMS = NTHREADS / TPR, ES = U == 4 ? 4 : 2, P = U / 2;
+    using TeamT = Team<TPR, WIDE>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t bars[TEAMS * MAX_SLOTS];
-    __shared__ __align__(16) float scratch_all[TEAMS * 8 * (TPR / 32)];
+    __shared__ __align__(16) float scratch[TEAMS * TeamT::SCRATCH];
     __shared__ int abort_all;
-    const int team = threadIdx.x / TPR, t = threadIdx.x % TPR;
-    const int C = a.C, NV = C / 4;
-    float* scratch = scratch_all + team * 8 * (TPR / 32);
+    const int t = threadIdx.x % TPR;
+    TeamT team;
+    team.index = threadIdx.x / TPR;
+    team.scratch = scratch + team.index * TeamT::SCRATCH;
+    team.phase = 0;
+    team.rank = WIDE ? cluster_ctarank() : 0;
+    team.ranks = WIDE ? cluster_nctarank() : 1;
+    const int c0 = first_column(a.cols, team.rank), cols = min(a.cols, a.C - c0), NU = cols / U;
     if (threadIdx.x == 0) abort_all = 0;
     if (threadIdx.x < TEAMS * MAX_SLOTS) mbar_init(smem_u32(&bars[threadIdx.x]), 1);
     fence_mbar_init();
     __syncthreads();
+    if constexpr (WIDE) cluster_sync();
     volatile int* abort_flag = &abort_all;
 
     const bool has_h = a.h != nullptr, has_dy = a.dy != nullptr;
-    const uint32_t res_bytes = (uint32_t)C * ES, half_bytes = (uint32_t)C * 2;
+    const uint32_t res_bytes = (uint32_t)cols * ES, half_bytes = (uint32_t)cols * 2;
     // a slot: y, dy (residual type), dz, h (bf16)
     const uint32_t at_dy = res_bytes, at_dz = at_dy + (has_dy ? res_bytes : 0), at_h = at_dz + half_bytes;
     const uint32_t row_bytes = at_h + (has_h ? half_bytes : 0);
-    uint8_t* ring = smem + (size_t)team * a.slots * a.slot_bytes;
-    const uint32_t ring_u = smem_u32(ring);
-    const int64_t team_id = blockIdx.x + (int64_t)gridDim.x * team, n_teams = (int64_t)gridDim.x * TEAMS;
+    const uint8_t* ring = smem + (size_t)team.index * a.slots * a.slot_bytes;
+    const uint32_t ring_u = smem_u32(ring), bars_u = smem_u32(&bars[team.index * MAX_SLOTS]);
+    const int64_t teams = (int64_t)(gridDim.x / team.ranks) * TEAMS;
+    const int64_t id = blockIdx.x / team.ranks + (int64_t)(gridDim.x / team.ranks) * team.index;
     const int64_t items = a.groups * a.parts;
-    auto item_begin = [&](int64_t item, int64_t& begin, int64_t& end) {
+    auto item_rows = [&](int64_t item, int64_t& begin, int64_t& end) {
         const int64_t g = item / a.parts, p = item - g * a.parts;
         begin = g * a.rows_per_group + a.rows_per_group * p / a.parts;
         end = g * a.rows_per_group + a.rows_per_group * (p + 1) / a.parts;
     };
-    // the rows ahead, over the items of this team
-    int64_t ahead_item = team_id, ahead = 0, ahead_end = 0;
-    if (ahead_item < items) item_begin(ahead_item, ahead, ahead_end);
-    auto fill_next = [&](int slot) {
-        while (ahead >= ahead_end) {
-            ahead_item += n_teams;
-            if (ahead_item >= items) {
-                ahead_item = items;
-                return;
-            }
-            item_begin(ahead_item, ahead, ahead_end);
-        }
+    // the rows ahead, over the items of this team (an item has a row at least)
+    int64_t ahead_item = id, ahead = 0, ahead_end = 0;
+    if (ahead_item < items) item_rows(ahead_item, ahead, ahead_end);
+    auto fill_next = [&](int slot) {  // by thread 0
+        if (ahead_item >= items) return;
         const int64_t row = ahead++;
-        const uint32_t bar = smem_u32(&bars[team * MAX_SLOTS + slot]);
-        const uint32_t at = ring_u + a.slot_bytes * slot;
+        const uint32_t bar = bars_u + 8u * slot, at = ring_u + a.slot_bytes * slot;
         mbar_arrive_expect_tx(bar, row_bytes);
-        bulk_load(at, static_cast<const uint8_t*>(a.y) + row * a.ldy * ES, res_bytes, bar);
-        if (has_dy) bulk_load(at + at_dy, static_cast<const uint8_t*>(a.dy) + row * a.lddy * ES, res_bytes, bar);
-        bulk_load(at + at_dz, a.dz + row * a.lddz, half_bytes, bar);
-        if (has_h) bulk_load(at + at_h, a.h + row * a.ldh, half_bytes, bar);
+        bulk_load(at, static_cast<const uint8_t*>(a.y) + (row * a.ldy + c0) * ES, res_bytes, bar);
+        if (has_dy) bulk_load(at + at_dy, static_cast<const uint8_t*>(a.dy) + (row * a.lddy + c0) * ES, res_bytes, bar);
+        bulk_load(at + at_dz, a.dz + row * a.lddz + c0, half_bytes, bar);
+        if (has_h) bulk_load(at + at_h, a.h + row * a.ldh + c0, half_bytes, bar);
+        if (ahead >= ahead_end && (ahead_item += teams) < items) item_rows(ahead_item, ahead, ahead_end);
     };
-    if (t == 0 && ahead_item < items)
-        for (int s = 0; s < a.slots && ahead_item < items; ++s) fill_next(s);
-    const float inv_c = 1.0f / (float)C;
-    int phase = 0, slot = 0;
+    if (t == 0)
+        for (int s = 0; s < a.slots; ++s) fill_next(s);
+    const float inv_c = 1.0f / (float)a.C;
+    int slot = 0, done = -1;  // done: the slot of the row before
     uint32_t parity = 0;
-    for (int64_t item = team_id; item < items; item += n_teams) {
+    for (int64_t item = id; item < items; item += teams) {
         int64_t begin, end;
-        item_begin(item, begin, end);
+        item_rows(item, begin, end);
         const int64_t group = item / a.parts;
-        float s_dz[J][4], s_dzn[J][4], s_dxm[J][4];
+        float2 A[J][P], B[J][P], s_dz[J][P], s_dzn[J][P], s_dxm[J][P];
 #pragma unroll
-        for (int j = 0; j < J; ++j)
+        for (int j = 0; j < J; ++j) {
+            const int u = t + TPR * j;
+            const bool on = u < NU;
+            const int64_t c = on ? c0 + U * u : 0;
+            float2 p[P], q[P];
+            load_vector<U>(a.gate, group * a.lgate + c, 1.0f, p);
+            load_vector<U>(a.post, c, 1.0f, q);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s_dz[j][i] = s_dzn[j][i] = s_dxm[j][i] = 0.0f;
-        for (int64_t row = begin; row < end; ++row) {
-            const bool ok = mbar_wait(smem_u32(&bars[team * MAX_SLOTS + slot]), parity, abort_flag, a.status, kLimitNs);
+            for (int i = 0; i < P; ++i) A[j][i] = on ? __fmul2_rn(p[i], q[i]) : both(0.0f);
+            load_vector<U>(a.pre, c, 1.0f, p);
+            load_vector<U>(a.scale, group * a.lscale + c, 0.0f, q);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                B[j][i] = on ? __ffma2_rn(p[i], q[i], p[i]) : both(0.0f);
+                s_dz[j][i] = s_dzn[j][i] = s_dxm[j][i] = both(0.0f);
+            }
+        }
+        uint8_t* dx_at = static_cast<uint8_t*>(a.dx) + (begin * a.lddx + c0) * ES;
+        __nv_bfloat16* dh_at = a.dh + (begin * a.lddh + c0);
+        for (int64_t row = begin; row < end; ++row, dx_at += a.lddx * ES, dh_at += a.lddh) {
+            const bool ok = mbar_wait(bars_u + 8u * slot, parity, abort_flag, a.status, kLimitNs);
             const uint8_t* at = ring + (size_t)a.slot_bytes * slot;
-            float y[J][4], dy[J][4];
-            uint2 dz[J], h[J];
-            // sums of the first pass: y, dn, h (layer norm), then their squares and dn y
-            float s1[3] = {0.0f, 0.0f, 0.0f};
+            Packed<U> dz[J], h[J];
+            float p = 0.0f, q = 0.0f;
+            if (LAYER) {
+                p = pivot_of<U>(at, cols);
+                if (has_h) q = pivot_of<8>(at + at_h, cols);
+                share_pivots(team, p, q);
+            }
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                const int v = t + TPR * j;
-                dz[j] = h[j] = make_uint2(0, 0);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y[j][i] = dy[j][i] = 0.0f;
-                if (v < NV) {
-                    if constexpr (F32) {
-                        const float4 f = reinterpret_cast<const float4*>(at)[v];
-                        y[j][0] = f.x, y[j][1] = f.y, y[j][2] = f.z, y[j][3] = f.w;
-                        if (has_dy) {
-                            const float4 d = reinterpret_cast<const float4*>(at + at_dy)[v];
-                            dy[j][0] = d.x, dy[j][1] = d.y, dy[j][2] = d.z, dy[j][3] = d.w;
-                        }
-                    } else {
-                        unpack4(reinterpret_cast<const uint2*>(at)[v], y[j]);
-                        if (has_dy) unpack4(reinterpret_cast<const uint2*>(at + at_dy)[v], dy[j]);
-                    }
-                    dz[j] = reinterpret_cast<const uint2*>(at + at_dz)[v];
-                    if (has_h) h[j] = reinterpret_cast<const uint2*>(at + at_h)[v];
+                const int u = t + TPR * j;
+                dz[j] = Packed<U>{};
+                h[j] = Packed<U>{};
+                if (u < NU) {
+                    dz[j] = reinterpret_cast<const Packed<U>*>(at + at_dz)[u];
+                    if (has_h) h[j] = reinterpret_cast<const Packed<U>*>(at + at_h)[u];
                 }
-                if (!ok)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) y[j][i] = __int_as_float(0x7FC00000);
             }
-            auto dn_of = [&](int j, float (&dn)[4], float (&d)[4]) {
-                // dz and dz pre (1 + scale)
-                const int v = t + TPR * j;
-                uint2 pw = make_uint2(0, 0), sw = make_uint2(0, 0);
-                if (v < NV) {
-                    pw = ldg8_or(a.pre, 4 * v, kOnes);
-                    sw = ldg8_or(a.scale, group * a.lscale + 4 * v, 0u);
-                }
-                float p[4], s[4];
-                unpack4(dz[j], d);
-                unpack4(pw, p);
-                unpack4(sw, s);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) dn[i] = d[i] * __fmaf_rn(p[i], s[i], p[i]);
-            };
-            float mean_y = 0.0f, mean_h = 0.0f, mean_dn = 0.0f;
-            if (a.layer) {
+            float ry, rh, mean_y = 0.0f, mean_h = 0.0f, mean_dn = 0.0f, c1;
+            for (int again = 0;; ++again) {
+                float2 s_y = both(0.0f), s_y2 = both(0.0f), s_dn = both(0.0f), s_dny = both(0.0f), s_h = both(0.0f),
+                       s_h2 = both(0.0f);
+                const float2 p2 = both(-p), q2 = both(-q);
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
-                    float dn[4], d[4], hh[4];
-                    dn_of(j, dn, d);
-                    unpack4(h[j], hh);
+                    const int u = t + TPR * j;
+                    if (u < NU) {
+                        float2 y[P], d[P], f[P];
+                        load_res(at, u, y);
+                        if (!ok) y[0].x = __int_as_float(0x7FC00000);  // a row that never came
+                        unpack(dz[j], d);
+                        unpack(h[j], f);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        s1[0] += y[j][i];
-                        s1[1] += dn[i];
-                        s1[2] += hh[i];
+                        for (int i = 0; i < P; ++i) {
+                            d[i] = __fmul2_rn(d[i], B[j][i]);
+                            if constexpr (LAYER) {
+                                y[i] = __fadd2_rn(y[i], p2);
+                                f[i] = __fadd2_rn(f[i], q2);
+                                s_y = __fadd2_rn(s_y, y[i]);
+                                s_h = __fadd2_rn(s_h, f[i]);
+                                s_dn = __fadd2_rn(s_dn, d[i]);
+                            }
+                            s_y2 = __ffma2_rn(y[i], y[i], s_y2);
+                            s_dny = __ffma2_rn(d[i], y[i], s_dny);
+                            s_h2 = __ffma2_rn(f[i], f[i], s_h2);
+                        }
                     }
                 }
-                team_sum<TPR, 3>(s1, scratch, phase, team);
-                mean_y = s1[0] * inv_c;
-                mean_dn = s1[1] * inv_c;
-                mean_h = s1[2] * inv_c;
+                if constexpr (!LAYER) {
+                    float s[3] = {s_y2.x + s_y2.y, s_dny.x + s_dny.y, s_h2.x + s_h2.y};
+                    team.sum(s);
+                    ry = rsqrtf(__fmaf_rn(s[0], inv_c, a.eps));
+                    rh = rsqrtf(__fmaf_rn(s[2], inv_c, a.eps));
+                    c1 = s[1] * inv_c * ry;  // mean(dn n)
+                    break;
+                } else {
+                    float s[6] = {s_y.x + s_y.y, s_y2.x + s_y2.y, s_dn.x + s_dn.y, s_dny.x + s_dny.y, s_h.x + s_h.y,
+                                  s_h2.x + s_h2.y};
+                    team.sum(s);
+                    const float d = s[0] * inv_c, e = s[4] * inv_c;
+                    const float vy = __fmaf_rn(-d, d, s[1] * inv_c), vh = __fmaf_rn(-e, e, s[5] * inv_c);
+                    mean_y = p + d;
+                    mean_h = q + e;
+                    mean_dn = s[2] * inv_c;
+                    ry = rsqrtf(fmaxf(vy, 0.0f) + a.eps);
+                    rh = rsqrtf(fmaxf(vh, 0.0f) + a.eps);
+                    c1 = (s[3] * inv_c - d * mean_dn) * ry;
+                    if (again || (d * d <= vy && e * e <= vh)) break;
+                    p = mean_y;
+                    q = mean_h;
+                }
             }
-            float s2[3] = {0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                float dn[4], d[4], hh[4];
-                dn_of(j, dn, d);
-                unpack4(h[j], hh);
-                if (t + TPR * j < NV)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        y[j][i] -= mean_y;
-                        s2[0] = __fmaf_rn(y[j][i], y[j][i], s2[0]);
-                        s2[1] = __fmaf_rn(dn[i], y[j][i], s2[1]);
-                        s2[2] = __fmaf_rn(hh[i] - mean_h, hh[i] - mean_h, s2[2]);
-                    }
-            }
-            team_sum<TPR, 3>(s2, scratch, phase, team);
-            if (t == 0 && ahead_item < items && !*abort_flag) fill_next(slot);
+            // the row before has left its slot
+            if (t == 0 && done >= 0 && !*abort_flag) fill_next(done);
+            done = slot;
             if (++slot == a.slots) {
                 slot = 0;
                 parity ^= 1;
             }
-            const float ry = rsqrtf(__fmaf_rn(s2[0], inv_c, a.eps)), rh = rsqrtf(__fmaf_rn(s2[2], inv_c, a.eps));
-            const float c1 = s2[1] * inv_c * ry;  // mean(dn n)
-            float s3[2] = {0.0f, 0.0f};
+            float2 dm[J][P];
+            float2 s_dmm = both(0.0f), s_dm = both(0.0f);
+            const float2 my2 = both(-mean_y), mh2 = both(-mean_h), ry2 = both(ry), rh2 = both(rh), c12 = both(-c1),
+                         md2 = both(-mean_dn);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                const int v = t + TPR * j;
-                float dn[4], d[4];
-                dn_of(j, dn, d);
-                uint2 pw = make_uint2(0, 0), gw = make_uint2(0, 0);
-                if (has_h && v < NV) {
-                    pw = ldg8_or(a.post, 4 * v, kOnes);
-                    gw = ldg8_or(a.gate, group * a.lgate + 4 * v, kOnes);
-                }
-                float p[4], g[4], hh[4];
-                unpack4(pw, p);
-                unpack4(gw, g);
-                unpack4(h[j], hh);
+                const int u = t + TPR * j;
+                if (u < NU) {
+                    float2 y[P], d[P], f[P], g[P];
+                    load_res(at, u, y);
+                    if (has_dy) {
+                        load_res(at + at_dy, u, g);
+                    } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float n = y[j][i] * ry;
-                    s_dz[j][i] += d[i];
-                    s_dzn[j][i] = __fmaf_rn(d[i], n, s_dzn[j][i]);
-                    const float dx = __fmaf_rn(ry, dn[i] - mean_dn - n * c1, dy[j][i]);
-                    const float m = (hh[i] - mean_h) * rh;
-                    s_dxm[j][i] = __fmaf_rn(dx, m, s_dxm[j][i]);
-                    const float dm = dx * (g[i] * p[i]);
-                    s3[0] = __fmaf_rn(dm, m, s3[0]);
-                    s3[1] += dm;
-                    dy[j][i] = dx;
-                    y[j][i] = dm;
-                }
-                if (v < NV && FP4ATTN_IN_BOUNDS(row < a.rows && 4 * v + 4 <= C, a.status)) {
-                    if constexpr (F32)
-                        *reinterpret_cast<float4*>(static_cast<float*>(a.dx) + row * a.lddx + 4 * v) =
-                            make_float4(dy[j][0], dy[j][1], dy[j][2], dy[j][3]);
-                    else
-                        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.dx) + row * a.lddx + 4 * v) =
-                            make_uint2(pack_bf16x2(dy[j][0], dy[j][1]), pack_bf16x2(dy[j][2], dy[j][3]));
+                        for (int i = 0; i < P; ++i) g[i] = both(0.0f);
+                    }
+                    unpack(dz[j], d);
+                    unpack(h[j], f);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        if (LAYER) y[i] = __fadd2_rn(y[i], my2);
+                        const float2 n = __fmul2_rn(y[i], ry2);
+                        s_dz[j][i] = __fadd2_rn(s_dz[j][i], d[i]);
+                        s_dzn[j][i] = __ffma2_rn(d[i], n, s_dzn[j][i]);
+                        float2 e = __ffma2_rn(n, c12, __fmul2_rn(d[i], B[j][i]));
+                        if (LAYER) e = __fadd2_rn(e, md2);
+                        g[i] = __ffma2_rn(e, ry2, g[i]);  // dx
+                        if (LAYER) f[i] = __fadd2_rn(f[i], mh2);
+                        const float2 m = __fmul2_rn(f[i], rh2);
+                        s_dxm[j][i] = __ffma2_rn(g[i], m, s_dxm[j][i]);
+                        dm[j][i] = __fmul2_rn(g[i], A[j][i]);
+                        s_dmm = __ffma2_rn(dm[j][i], m, s_dmm);
+                        if (LAYER) s_dm = __fadd2_rn(s_dm, dm[j][i]);
+                    }
+                    if (FP4ATTN_IN_BOUNDS(row < a.rows && c0 + U * u + U <= a.C, a.status)) store_res(dx_at, u, g);
                 }
             }
             if (!has_h) continue;
-            team_sum<TPR, 2>(s3, scratch, phase, team);
-            const float c2 = s3[0] * inv_c, mean_dm = a.layer ? s3[1] * inv_c : 0.0f;
+            float c2, mean_dm = 0.0f;
+            if constexpr (LAYER) {
+                float s[2] = {s_dmm.x + s_dmm.y, s_dm.x + s_dm.y};
+                team.sum(s);
+                c2 = s[0] * inv_c;
+                mean_dm = s[1] * inv_c;
+            } else {
+                float s[1] = {s_dmm.x + s_dmm.y};
+                team.sum(s);
+                c2 = s[0] * inv_c;
+            }
+            const float2 c22 = both(-c2), mdm2 = both(-mean_dm);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                const int v = t + TPR * j;
-                float hh[4], o[4];
-                unpack4(h[j], hh);
+                const int u = t + TPR * j;
+                if (u < NU) {
+                    float2 f[P];
+                    unpack(h[j], f);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float m = (hh[i] - mean_h) * rh;
-                    o[i] = rh * (y[j][i] - mean_dm - m * c2);
+                    for (int i = 0; i < P; ++i) {
+                        if (LAYER) f[i] = __fadd2_rn(f[i], mh2);
+                        float2 e = __ffma2_rn(__fmul2_rn(f[i], rh2), c22, dm[j][i]);
+                        if (LAYER) e = __fadd2_rn(e, mdm2);
+                        f[i] = __fmul2_rn(e, rh2);
+                    }
+                    if (FP4ATTN_IN_BOUNDS(row < a.rows && c0 + U * u + U <= a.C, a.status))
+                        reinterpret_cast<Packed<U>*>(dh_at)[u] = pack(f);
                 }
-                if (v < NV && FP4ATTN_IN_BOUNDS(row < a.rows && 4 * v + 4 <= C, a.status))
-                    *reinterpret_cast<uint2*>(a.dh + row * a.lddh + 4 * v) =
-                        make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
             }
         }
-        float* part = a.part + item * 3 * (int64_t)C;
+        float* part = a.part + item * 3 * (int64_t)a.C + c0;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const int v = t + TPR * j;
-            if (v < NV && FP4ATTN_IN_BOUNDS(item < items, a.status)) {
-                reinterpret_cast<float4*>(part)[v] = make_float4(s_dz[j][0], s_dz[j][1], s_dz[j][2], s_dz[j][3]);
-                reinterpret_cast<float4*>(part + C)[v] = make_float4(s_dzn[j][0], s_dzn[j][1], s_dzn[j][2], s_dzn[j][3]);
-                reinterpret_cast<float4*>(part + 2 * C)[v] =
-                    make_float4(s_dxm[j][0], s_dxm[j][1], s_dxm[j][2], s_dxm[j][3]);
+            const int u = t + TPR * j;
+            if (u < NU && FP4ATTN_IN_BOUNDS(item < items, a.status)) {
+#pragma unroll
+                for (int i = 0; i < P; i += 2) {
+                    const int c = U * u + 2 * i;
+                    *reinterpret_cast<float4*>(part + c) =
+                        make_float4(s_dz[j][i].x, s_dz[j][i].y, s_dz[j][i + 1].x, s_dz[j][i + 1].y);
+                    *reinterpret_cast<float4*>(part + a.C + c) =
+                        make_float4(s_dzn[j][i].x, s_dzn[j][i].y, s_dzn[j][i + 1].x, s_dzn[j][i + 1].y);
+                    *reinterpret_cast<float4*>(part + 2 * (int64_t)a.C + c) =
+                        make_float4(s_dxm[j][i].x, s_dxm[j][i].y, s_dxm[j][i + 1].x, s_dxm[j][i + 1].y);
+                }
             }
         }
     }
     if (t == 0 && *abort_flag) {
         int dummy = 0;
         for (int s = 0; s < a.slots; ++s)
-            for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait(smem_u32(&bars[team * MAX_SLOTS + s]), ph, &dummy, nullptr, 200000000ull);
+            for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait(bars_u + 8u * s, ph, &dummy, nullptr, kDrainNs);
     }
 }
 
@@ -626,103 +805,119 @@ __global__ void __launch_bounds__(256) norm_weights_kernel(const __grid_constant
     if (a.dpost) a.dpost[c] = s[1];
 }
 
-constexpr size_t RING_BYTES = 160 * 1024;  // shared memory of the rings; the rest of the 228 KB serves as L1 for the vectors
-constexpr size_t RING_MOST = 200 * 1024;
+constexpr size_t RING_BYTES = 222 * 1024;
+// the backward fills a slot one row late: it needs two at its widest rows
+static_assert(2 * 12 * (size_t)NTHREADS * MAX_VALUES <= RING_BYTES, "two slots of the widest rows");
 
-// Slots per team: as many as fit RING_BYTES, at most MAX_SLOTS; two where
-// RING_MOST holds them, else one.
-int ring_slots(size_t row_bytes, int teams) {
-    int s = (int)(RING_BYTES / (row_bytes * teams));
-    if (s > MAX_SLOTS) s = MAX_SLOTS;
-    if (s < 2) s = row_bytes * teams * 2 <= RING_MOST ? 2 : 1;
+// How a row of C channels is shared out: CTAs of a cluster, threads of a CTA
+// per row, values per thread in eights.
+struct Split {
+    int ctas, cols, tpr, j8;
+};
+Split split_of(int64_t C) {
+    Split s{1, (int)C, NTHREADS, 0};
+    const int64_t most = NTHREADS * MAX_VALUES;
+    if (C > most) {
+        s.ctas = C > 2 * most ? MAX_CLUSTER : 2;
+        s.cols = (int)((C + 64 * s.ctas - 1) / (64 * s.ctas) * 64);
+    }
+    while (s.tpr > 32 && s.cols <= s.tpr / 2 * MAX_VALUES) s.tpr /= 2;
+    s.j8 = (s.cols + 8 * s.tpr - 1) / (8 * s.tpr);
     return s;
 }
 
-int sm_count(int& sms) {
-    int dev = 0;
+// A launch on the device's SMs: clusters that fit at once, ring slots and
+// shared memory.  Every field is set, or the status returned.
+struct Shape {
+    unsigned grid;
+    int slots;
+    size_t smem;
+};
+int shape_of(const void* kernel, const Split& s, size_t slot_bytes, int64_t work, Shape& sh) {
+    const int teams = NTHREADS / s.tpr;
+    sh.slots = (int)(RING_BYTES / (slot_bytes * teams));
+    sh.slots = sh.slots < 1 ? 1 : sh.slots > MAX_SLOTS ? MAX_SLOTS : sh.slots;
+    sh.smem = slot_bytes * teams * sh.slots;
+    int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh.smem) != cudaSuccess)
         return FP4ATTN_ERR_CUDA;
+    int64_t clusters = sms / s.ctas;
+    clusters = clusters < work ? clusters : work;
+    sh.grid = (unsigned)(clusters * s.ctas);
     return FP4ATTN_OK;
 }
 
-template <int TPR, int J, bool F32, bool QUANT>
-int launch_fwd(NormArgs a, cudaStream_t stream) {
-    constexpr int TEAMS = NTHREADS / TPR;
-    int sms = 0;
-    if (sm_count(sms) != FP4ATTN_OK) return FP4ATTN_ERR_CUDA;
-    const size_t row = (size_t)a.C * ((F32 ? 4 : 2) + (a.h ? 2 : 0));
-    a.slot_bytes = (uint32_t)row;
-    a.slots = ring_slots(row, TEAMS);
-    const size_t smem = row * TEAMS * a.slots;
-    auto kernel = norm_gate_kernel<TPR, J, F32, QUANT>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return FP4ATTN_ERR_CUDA;
-    const int64_t grid = a.rows < sms ? a.rows : sms;
-    kernel<<<(unsigned)grid, NTHREADS, smem, stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? FP4ATTN_OK : FP4ATTN_ERR_CUDA;
-}
-
-template <int TPR, int J>
-int launch_fwd_types(const NormArgs& a, bool f32, cudaStream_t stream) {
-    if (a.codes) return f32 ? launch_fwd<TPR, J, true, true>(a, stream) : launch_fwd<TPR, J, false, true>(a, stream);
-    return f32 ? launch_fwd<TPR, J, true, false>(a, stream) : launch_fwd<TPR, J, false, false>(a, stream);
-}
-
-template <int TPR, int J>
-int launch_bwd(NormBwdArgs a, bool f32, cudaStream_t stream) {
-    constexpr int TEAMS = NTHREADS / TPR;
-    int sms = 0;
-    if (sm_count(sms) != FP4ATTN_OK) return FP4ATTN_ERR_CUDA;
-    const size_t res = (size_t)a.C * (f32 ? 4 : 2);
-    const size_t row = res * (a.dy ? 2 : 1) + (size_t)a.C * (a.h ? 4 : 2);
-    a.slot_bytes = (uint32_t)row;
-    a.slots = ring_slots(row, TEAMS);
-    const size_t smem = row * TEAMS * a.slots;
-    auto kernel = f32 ? norm_gate_bwd_kernel<TPR, J, true> : norm_gate_bwd_kernel<TPR, J, false>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return FP4ATTN_ERR_CUDA;
-    const int64_t items = a.groups * a.parts;
-    const int64_t grid = items < sms ? items : sms;
-    kernel<<<(unsigned)grid, NTHREADS, smem, stream>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return FP4ATTN_ERR_CUDA;
-    const int64_t blocks = (a.C + 31) / 32;
-    norm_join_kernel<<<(unsigned)(blocks * a.groups), 256, 0, stream>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return FP4ATTN_ERR_CUDA;
-    if (a.groups > 1 && (a.dpre || a.dpost)) {
-        norm_weights_kernel<<<(unsigned)blocks, 256, 0, stream>>>(a);
-        if (cudaGetLastError() != cudaSuccess) return FP4ATTN_ERR_CUDA;
+template <typename Args>
+int launch(void (*kernel)(Args), const Args& a, const Split& s, const Shape& sh, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(sh.grid);
+    cfg.blockDim = dim3(NTHREADS);
+    cfg.dynamicSmemBytes = sh.smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    if (s.ctas > 1) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)s.ctas;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
     }
-    return FP4ATTN_OK;
+    return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? FP4ATTN_OK : FP4ATTN_ERR_CUDA;
 }
 
-int bwd_threads_per_row(int64_t C) { return C <= 512 ? 32 : C <= 1024 ? 64 : C <= 2048 ? 128 : C <= 4096 ? 256 : 512; }
+using FwdKernel = void (*)(const NormArgs);
+using BwdKernel = void (*)(const NormBwdArgs);
+
+template <int TPR, int J8, bool WIDE>
+FwdKernel fwd_of(bool f32, bool layer, bool quant) {
+    if (f32) {
+        if (layer)
+            return quant ? norm_gate_kernel<TPR, 2 * J8, 4, true, true, WIDE> : norm_gate_kernel<TPR, 2 * J8, 4, true, false, WIDE>;
+        return quant ? norm_gate_kernel<TPR, 2 * J8, 4, false, true, WIDE> : norm_gate_kernel<TPR, 2 * J8, 4, false, false, WIDE>;
+    }
+    if (layer) return quant ? norm_gate_kernel<TPR, J8, 8, true, true, WIDE> : norm_gate_kernel<TPR, J8, 8, true, false, WIDE>;
+    return quant ? norm_gate_kernel<TPR, J8, 8, false, true, WIDE> : norm_gate_kernel<TPR, J8, 8, false, false, WIDE>;
+}
+template <int TPR, int J8, bool WIDE>
+BwdKernel bwd_of(bool f32, bool layer, bool) {
+    if (f32) return layer ? norm_gate_bwd_kernel<TPR, 2 * J8, 4, true, WIDE> : norm_gate_bwd_kernel<TPR, 2 * J8, 4, false, WIDE>;
+    return layer ? norm_gate_bwd_kernel<TPR, J8, 8, true, WIDE> : norm_gate_bwd_kernel<TPR, J8, 8, false, WIDE>;
+}
+
+// Teams of 32 threads take 1 to 3 eights a thread, larger ones 2 or 3 (fewer
+// than that fits a team of half the size).
+#define FP4ATTN_NORM_KERNEL(of, s, f32, layer, quant)                                                                  \
+    ((s).ctas > 1    ? ((s).j8 <= 2 ? of<256, 2, true>(f32, layer, quant) : of<256, 3, true>(f32, layer, quant))       \
+     : (s).tpr == 32 ? ((s).j8 == 1   ? of<32, 1, false>(f32, layer, quant)                                            \
+                        : (s).j8 == 2 ? of<32, 2, false>(f32, layer, quant)                                            \
+                                      : of<32, 3, false>(f32, layer, quant))                                           \
+     : (s).tpr == 64 ? ((s).j8 <= 2 ? of<64, 2, false>(f32, layer, quant) : of<64, 3, false>(f32, layer, quant))       \
+     : (s).tpr == 128 ? ((s).j8 <= 2 ? of<128, 2, false>(f32, layer, quant) : of<128, 3, false>(f32, layer, quant))    \
+                      : ((s).j8 <= 2 ? of<256, 2, false>(f32, layer, quant) : of<256, 3, false>(f32, layer, quant)))
 
 }  // namespace
 
-int launch_norm_gate(const NormArgs& a, bool f32, cudaStream_t stream) {
-    const int NV = a.C / 8;
-    switch ((NV + 31) / 32) {
-        case 1: return launch_fwd_types<32, 1>(a, f32, stream);
-        case 2: return launch_fwd_types<32, 2>(a, f32, stream);
-        case 3: return launch_fwd_types<32, 3>(a, f32, stream);
-        case 4: return launch_fwd_types<32, 4>(a, f32, stream);
-    }
-    if (NV <= 64 * 3) return launch_fwd_types<64, 3>(a, f32, stream);
-    if (NV <= 64 * 4) return launch_fwd_types<64, 4>(a, f32, stream);
-    if (NV <= 128 * 3) return launch_fwd_types<128, 3>(a, f32, stream);
-    if (NV <= 128 * 4) return launch_fwd_types<128, 4>(a, f32, stream);
-    if (NV <= 256 * 3) return launch_fwd_types<256, 3>(a, f32, stream);
-    if (NV <= 256 * 4) return launch_fwd_types<256, 4>(a, f32, stream);
-    if (NV <= 512 * 3) return launch_fwd_types<512, 3>(a, f32, stream);
-    return launch_fwd_types<512, 4>(a, f32, stream);
+int launch_norm_gate(const NormArgs& a0, bool f32, cudaStream_t stream) {
+    NormArgs a = a0;
+    const Split s = split_of(a.C);
+    const FwdKernel kernel = FP4ATTN_NORM_KERNEL(fwd_of, s, f32, a.layer, a.codes != nullptr);
+    a.cols = s.cols;
+    a.slot_bytes = (uint32_t)s.cols * ((f32 ? 4 : 2) + (a.h ? 2 : 0));
+    Shape sh;
+    const int st = shape_of(reinterpret_cast<const void*>(kernel), s, a.slot_bytes, a.rows, sh);
+    if (st != FP4ATTN_OK) return st;
+    a.slots = sh.slots;
+    return launch(kernel, a, s, sh, stream);
 }
 
 // Parts of a sample's rows: the longest work of a team, ceil(groups * parts /
 // teams) items of ceil(rows / parts) rows, is what the launch takes.
 int64_t norm_backward_parts(int64_t rows, int64_t C, int64_t groups) {
     if (rows == 0 || groups == 0) return 1;
-    const int64_t rpg = rows / groups, teams = 148 * (NTHREADS / bwd_threads_per_row(C));
+    const Split s = split_of(C);
+    const int64_t rpg = rows / groups, teams = 148 / s.ctas * (NTHREADS / s.tpr);
     int64_t most = (4 * teams + groups - 1) / groups;
     if (most > rpg) most = rpg;
     int64_t best = 1, cost = -1;
@@ -736,22 +931,25 @@ int64_t norm_backward_parts(int64_t rows, int64_t C, int64_t groups) {
     return best;
 }
 
-int launch_norm_gate_backward(const NormBwdArgs& a, bool f32, cudaStream_t stream) {
-    const int NV = a.C / 4, tpr = bwd_threads_per_row(a.C);
-    const int J = (NV + tpr - 1) / tpr;
-    switch (tpr) {
-        case 32:
-            if (J == 1) return launch_bwd<32, 1>(a, f32, stream);
-            if (J == 2) return launch_bwd<32, 2>(a, f32, stream);
-            return launch_bwd<32, 4>(a, f32, stream);
-        case 64: return J == 3 ? launch_bwd<64, 3>(a, f32, stream) : launch_bwd<64, 4>(a, f32, stream);
-        case 128: return J == 3 ? launch_bwd<128, 3>(a, f32, stream) : launch_bwd<128, 4>(a, f32, stream);
-        case 256: return J == 3 ? launch_bwd<256, 3>(a, f32, stream) : launch_bwd<256, 4>(a, f32, stream);
+int launch_norm_gate_backward(const NormBwdArgs& a0, bool f32, cudaStream_t stream) {
+    NormBwdArgs a = a0;
+    const Split s = split_of(a.C);
+    const BwdKernel kernel = FP4ATTN_NORM_KERNEL(bwd_of, s, f32, a.layer, false);
+    a.cols = s.cols;
+    a.slot_bytes = (uint32_t)s.cols * ((f32 ? 4 : 2) * (a.dy ? 2 : 1) + (a.h ? 4 : 2));
+    Shape sh;
+    const int st = shape_of(reinterpret_cast<const void*>(kernel), s, a.slot_bytes, a.groups * a.parts, sh);
+    if (st != FP4ATTN_OK) return st;
+    a.slots = sh.slots;
+    if (launch(kernel, a, s, sh, stream) != FP4ATTN_OK) return FP4ATTN_ERR_CUDA;
+    const int64_t blocks = (a.C + 31) / 32;
+    norm_join_kernel<<<(unsigned)(blocks * a.groups), 256, 0, stream>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return FP4ATTN_ERR_CUDA;
+    if (a.groups > 1 && (a.dpre || a.dpost)) {
+        norm_weights_kernel<<<(unsigned)blocks, 256, 0, stream>>>(a);
+        if (cudaGetLastError() != cudaSuccess) return FP4ATTN_ERR_CUDA;
     }
-    if (J == 3) return launch_bwd<512, 3>(a, f32, stream);
-    if (J == 4) return launch_bwd<512, 4>(a, f32, stream);
-    if (J <= 6) return launch_bwd<512, 6>(a, f32, stream);
-    return launch_bwd<512, 8>(a, f32, stream);
+    return FP4ATTN_OK;
 }
 
 }  // namespace fp4attn
