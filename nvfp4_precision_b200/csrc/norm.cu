@@ -19,10 +19,10 @@
 //   * The rows ahead come in by bulk copies into a ring in shared memory, one
 //     ring per team, so loads stay in flight through reductions and stores.
 //   * Two reductions over the team per row, for the layer norm too: its
-//     variance is taken about a pivot (the mean of eight values of the row)
-//     together with the mean, and again about that mean in the rare row whose
-//     pivot lay more than a standard deviation off, where the difference of
-//     squares would lose bits; y's mean follows from sums of the first pass.
+//     variance is taken about a pivot (the mean of eight values of the row; for
+//     y, of x) together with the mean, and again about that mean in the rare
+//     row whose pivot lay more than a standard deviation off, where the
+//     difference of squares would lose bits.
 // The forward's z can leave as NVFP4 rows (rounded to bf16 first, as the
 // quantiser of a bf16 z would see it), so that the next linear layer reads
 // 9/16 byte a value instead of writing, reading and quantising 2-byte ones.
@@ -64,6 +64,18 @@ __device__ __forceinline__ uint4 pack(const float2 (&v)[4]) {
 __device__ __forceinline__ uint2 pack(const float2 (&v)[2]) { return make_uint2(pack_pair(v[0]), pack_pair(v[1])); }
 __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
+// Largest magnitudes of a unit of bf16 values, a pair in a word, NaN kept.
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
+    uint32_t m;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+    return m;
+}
+__device__ __forceinline__ uint32_t abs_pair(uint32_t a) { return a & 0x7FFF7FFFu; }
+__device__ __forceinline__ uint32_t amax_pair(uint2 w) { return max_pair(abs_pair(w.x), abs_pair(w.y)); }
+__device__ __forceinline__ uint32_t amax_pair(uint4 w) {
+    return max_pair(amax_pair(make_uint2(w.x, w.y)), amax_pair(make_uint2(w.z, w.w)));
+}
+
 // Residual units in shared or global memory.
 __device__ __forceinline__ void load_res(const void* row, int u, float2 (&v)[4]) {
     unpack(static_cast<const uint4*>(row)[u], v);
@@ -76,12 +88,6 @@ __device__ __forceinline__ void store_res(void* row, int u, const float2 (&v)[4]
 __device__ __forceinline__ void store_res(void* row, int u, const float2 (&v)[2]) {
     static_cast<float4*>(row)[u] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
 }
-template <int U>
-__device__ __forceinline__ float res_value(const void* row, int i) {
-    if constexpr (U == 8) return __bfloat162float(static_cast<const __nv_bfloat16*>(row)[i]);
-    return static_cast<const float*>(row)[i];
-}
-
 // The values of a unit of a bf16 vector, or `absent` for a null one.
 template <int U>
 __device__ __forceinline__ void load_vector(const __nv_bfloat16* p, int64_t at, float absent, float2 (&v)[U / 2]) {
@@ -144,6 +150,12 @@ struct Team {
                 float s = 0.0f;
                 if constexpr (WIDE) {
                     for (int w = 0; w < (int)ranks * W; ++w) s += at[k * MAX_PARTS + w];
+                } else if constexpr (W >= 4) {
+#pragma unroll
+                    for (int w = 0; w < W; w += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(at + k * MAX_PARTS + w);
+                        s += (f.x + f.y) + (f.z + f.w);
+                    }
                 } else {
 #pragma unroll
                     for (int w = 0; w < W; ++w) s += at[k * MAX_PARTS + w];
@@ -157,13 +169,28 @@ struct Team {
 // The columns of a CTA: all of them, or a share of whole 64-channel chunks.
 __device__ __forceinline__ int first_column(int cols_per_cta, uint32_t rank) { return cols_per_cta * (int)rank; }
 
-// Mean of eight values spread over the row (of this CTA's columns).
-template <int U>
-__device__ __forceinline__ float pivot_of(const void* row, int cols) {
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s += res_value<U>(row, (int)((unsigned)cols * (unsigned)i / 8u));
-    return 0.125f * s;
+// Mean of eight neighbouring values in the middle of the row (of this CTA's
+// columns): of a residual (8: bf16, 4: fp32) or (2) of bf16 values in fours.
+template <int KIND>
+__device__ __forceinline__ float pivot_of(const void* row, int units) {
+    float2 s;
+    if constexpr (KIND == 8) {
+        float2 v[4];
+        load_res(row, units >> 1, v);
+        s = __fadd2_rn(__fadd2_rn(v[0], v[1]), __fadd2_rn(v[2], v[3]));
+    } else {
+        float2 v[2], w[2];
+        const int u = units >> 1;  // an even number of units: eight channels make two
+        if constexpr (KIND == 4) {
+            load_res(row, u - 1, v);
+            load_res(row, u, w);
+        } else {
+            unpack(static_cast<const uint2*>(row)[u - 1], v);
+            unpack(static_cast<const uint2*>(row)[u], w);
+        }
+        s = __fadd2_rn(__fadd2_rn(v[0], v[1]), __fadd2_rn(w[0], w[1]));
+    }
+    return 0.125f * (s.x + s.y);
 }
 // The same pivot for every CTA of a cluster.
 template <int TPR, bool WIDE>
@@ -177,15 +204,24 @@ __device__ __forceinline__ void share_pivots(Team<TPR, WIDE>& team, float& p, fl
 }
 
 // ------------------------------------------------------------- forward --
+//
+// The products of the vectors (A = gate post_weight, B = pre_weight
+// (1 + scale), S = shift) stand in shared memory, shared by the CTA's teams,
+// which take turns down the rows of one sample after another; that leaves
+// registers for 512 threads, twice the warps of the backward to hide the
+// reductions and the quantiser behind.
+
+constexpr int FWD_THREADS = 512;
 
 template <int TPR, int J, int U, bool LAYER, bool QUANT, bool WIDE>
-__global__ void __launch_bounds__(NTHREADS, 1) norm_gate_kernel(const __grid_constant__ NormArgs a) {
-    constexpr int TEAMS = NTHREADS / TPR, ES = U == 4 ? 4 : 2, P = U / 2;
+__global__ void __launch_bounds__(FWD_THREADS, 1) norm_gate_kernel(const __grid_constant__ NormArgs a) {
+    constexpr int TEAMS = WIDE ? 1 : FWD_THREADS / TPR, ES = U == 4 ? 4 : 2, P = U / 2;
     using TeamT = Team<TPR, WIDE>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t bars[TEAMS * MAX_SLOTS];
     __shared__ __align__(16) float scratch[TEAMS * TeamT::SCRATCH];
     __shared__ int abort_all;
+    __shared__ ScaleTable table;  // not used (and not there) unless QUANT
     const int t = threadIdx.x % TPR;
     TeamT team;
     team.index = threadIdx.x / TPR;
@@ -194,268 +230,271 @@ __global__ void __launch_bounds__(NTHREADS, 1) norm_gate_kernel(const __grid_con
     team.rank = WIDE ? cluster_ctarank() : 0;
     team.ranks = WIDE ? cluster_nctarank() : 1;
     const int c0 = first_column(a.cols, team.rank), cols = min(a.cols, a.C - c0), NU = cols / U;
+    const float gz = QUANT ? (a.gz ? __ldg(a.gz) : 1.0f) : 1.0f;
+    if (QUANT) make_scale_table(table, gz, threadIdx.x);
     if (threadIdx.x == 0) abort_all = 0;
     if (threadIdx.x < TEAMS * MAX_SLOTS) mbar_init(smem_u32(&bars[threadIdx.x]), 1);
     fence_mbar_init();
     __syncthreads();
     if constexpr (WIDE) cluster_sync();
     volatile int* abort_flag = &abort_all;
+    const float guess = QUANT ? table.guess : 0.0f;
+    if (QUANT && blockIdx.x == 0 && threadIdx.x == 0 && bad_gscale(gz)) raise_status(a.status, FP4ATTN_ERR_RANGE);
 
     const bool has_h = a.h != nullptr;
     const uint32_t x_bytes = (uint32_t)cols * ES, h_bytes = has_h ? (uint32_t)cols * 2 : 0;
-    const uint8_t* ring = smem + (size_t)team.index * a.slots * a.slot_bytes;
+    // four channels of each of A, B and S per entry: a unit of eight takes one from
+    // either half, so that the threads of a warp read consecutive entries
+    float4* vectors = reinterpret_cast<float4*>(smem);
+    const int plane = a.cols / U;  // entries; A, B, S of U / 4 planes each
+    const uint8_t* ring = smem + (size_t)12 * a.cols + (size_t)team.index * a.slots * a.slot_bytes;
     const uint32_t ring_u = smem_u32(ring), bars_u = smem_u32(&bars[team.index * MAX_SLOTS]);
-    const int64_t teams = (int64_t)(gridDim.x / team.ranks) * TEAMS;
-    const int64_t id = blockIdx.x / team.ranks + (int64_t)(gridDim.x / team.ranks) * team.index;
-    const int64_t r0 = a.rows * id / teams, r1 = a.rows * (id + 1) / teams;
-    const uint8_t* x_at = static_cast<const uint8_t*>(a.x) + (r0 * a.ldx + c0) * ES;
-    const __nv_bfloat16* h_at = a.h + (r0 * a.ldh + c0);
-    auto fill = [&](int slot) {  // of the next row, by thread 0
+    const int64_t clusters = gridDim.x / team.ranks, cluster = blockIdx.x / team.ranks;
+    const int64_t r0 = a.rows * cluster / clusters, r1 = a.rows * (cluster + 1) / clusters;
+    int64_t next = r0 + team.index;  // rows r0 + index, + TEAMS, ...
+    auto fill = [&](int slot) {      // of the next row, by thread 0
         const uint32_t bar = bars_u + 8u * slot, at = ring_u + a.slot_bytes * slot;
         mbar_arrive_expect_tx(bar, x_bytes + h_bytes);
-        bulk_load(at, x_at, x_bytes, bar);
-        x_at += a.ldx * ES;
-        if (has_h) {
-            bulk_load(at + x_bytes, h_at, h_bytes, bar);
-            h_at += a.ldh;
-        }
+        bulk_load(at, static_cast<const uint8_t*>(a.x) + (next * a.ldx + c0) * ES, x_bytes, bar);
+        if (has_h) bulk_load(at + x_bytes, a.h + next * a.ldh + c0, h_bytes, bar);
+        next += TEAMS;
     };
-    int64_t next = r0;
     if (t == 0)
-        for (int s = 0; s < a.slots && next < r1; ++s, ++next) fill(s);
-    const float gz = QUANT ? (a.gz ? __ldg(a.gz) : 1.0f) : 1.0f;
-    if (QUANT && blockIdx.x == 0 && threadIdx.x == 0 && bad_gscale(gz)) raise_status(a.status, FP4ATTN_ERR_RANGE);
+        for (int s = 0; s < a.slots && next < r1; ++s) fill(s);
     const float inv_c = 1.0f / (float)a.C;
-
-    // gate post_weight, pre_weight (1 + scale) and shift of this thread's channels
-    float2 A[J][P], B[J][P], S[J][P];
-    float mean_A = 0.0f;
-    int64_t group = r0 < r1 ? r0 / a.rows_per_group : 0;
-    int64_t group_end = group * a.rows_per_group;  // none loaded yet
+    const int sf_shift = 8 * ((t * U / 16) & 3);  // TPR U channels are whole chunks of 64
 
     bool finite = true;
     int slot = 0;
     uint32_t parity = 0;
-    uint8_t* y_at = static_cast<uint8_t*>(a.y) + (r0 * a.ldy + c0) * ES;
-    __nv_bfloat16* z_at = a.z + (r0 * a.ldz + c0);
-    for (int64_t row = r0; row < r1; ++row, y_at += a.ldy * ES, z_at += a.ldz) {
-        if (row >= group_end) {
-            if (row > r0) ++group;
-            group_end += a.rows_per_group;
-            if (row == r0) group_end = (group + 1) * a.rows_per_group;
-            float s[1] = {0.0f};
+    int64_t row = r0 + team.index;
+    for (int64_t group = r0 / a.rows_per_group; group * a.rows_per_group < r1; ++group) {
+        __syncthreads();
+        for (int u = threadIdx.x; u < NU; u += blockDim.x) {
+            const int64_t c = c0 + U * u;
+            float2 p[P], q[P];
+            auto put = [&](int which) {
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const int u = t + TPR * j;
-                const bool on = u < NU;
-                const int64_t c = on ? c0 + U * u : 0;
-                float2 p[P], q[P];
-                load_vector<U>(a.gate, group * a.lgate + c, 1.0f, p);
-                load_vector<U>(a.post, c, 1.0f, q);
+                for (int k = 0; k < U / 4; ++k)
+                    vectors[(which * (U / 4) + k) * plane + u] = make_float4(p[2 * k].x, p[2 * k].y, p[2 * k + 1].x, p[2 * k + 1].y);
+            };
+            load_vector<U>(a.gate, group * a.lgate + c, 1.0f, p);
+            load_vector<U>(a.post, c, 1.0f, q);
 #pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    A[j][i] = on ? __fmul2_rn(p[i], q[i]) : both(0.0f);
-                    s[0] += A[j][i].x + A[j][i].y;
-                }
-                load_vector<U>(a.pre, c, 1.0f, p);
-                load_vector<U>(a.scale, group * a.lscale + c, 0.0f, q);
+            for (int i = 0; i < P; ++i) p[i] = __fmul2_rn(p[i], q[i]);
+            put(0);
+            load_vector<U>(a.pre, c, 1.0f, p);
+            load_vector<U>(a.scale, group * a.lscale + c, 0.0f, q);
 #pragma unroll
-                for (int i = 0; i < P; ++i) B[j][i] = on ? __ffma2_rn(p[i], q[i], p[i]) : both(0.0f);
-                load_vector<U>(a.shift, group * a.lshift + c, 0.0f, p);
+            for (int i = 0; i < P; ++i) p[i] = __ffma2_rn(p[i], q[i], p[i]);
+            put(1);
+            load_vector<U>(a.shift, group * a.lshift + c, 0.0f, p);
+            put(2);
+        }
+        __syncthreads();
+        auto vector = [&](int which, int u, float2(&v)[P]) {
 #pragma unroll
-                for (int i = 0; i < P; ++i) S[j][i] = on ? p[i] : both(0.0f);
+            for (int k = 0; k < U / 4; ++k) {
+                const float4 f = vectors[(which * (U / 4) + k) * plane + u];
+                v[2 * k] = make_float2(f.x, f.y);
+                v[2 * k + 1] = make_float2(f.z, f.w);
             }
+        };
+        const int64_t end = min((group + 1) * a.rows_per_group, r1);
+        for (; row < end; row += TEAMS) {
+            const bool ok = mbar_wait(bars_u + 8u * slot, parity, abort_flag, a.status, kLimitNs);
+            const uint8_t* at = ring + (size_t)a.slot_bytes * slot;
+            // the pivots of y (a guess from x) and h; channels past the row's end
+            // hold them and add nothing
+            float p = 0.0f, q = 0.0f;
             if (LAYER) {
-                team.sum(s);
-                mean_A = s[0] * inv_c;
+                p = pivot_of<U>(at, NU);
+                if (has_h) q = pivot_of<U == 8 ? 8 : 2>(at + x_bytes, NU);
+                share_pivots(team, p, q);
             }
-        }
-        const bool ok = mbar_wait(bars_u + 8u * slot, parity, abort_flag, a.status, kLimitNs);
-        const uint8_t* at = ring + (size_t)a.slot_bytes * slot;
-        float2 y[J][P];
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int u = t + TPR * j;
-            if (u < NU) {
-                load_res(at, u, y[j]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < P; ++i) y[j][i] = both(0.0f);
-            }
-            // a row that never came (its wait ran out) must not pass for one
-            if (!ok) y[j][0].x = __int_as_float(0x7FC00000);
-        }
-        float mean = 0.0f;  // of y: where its sums are taken about
-        if (has_h) {
+            const uint32_t q_word = pack_bf16x2(q, q);
+            if (LAYER) q = bf16lo(q_word);
+            float2 y[J][P];
             Packed<U> h[J];
-            float q = 0.0f, unused = 0.0f;
-            if (LAYER) {
-                q = pivot_of<8>(at + x_bytes, cols);
-                share_pivots(team, q, unused);
-            }
-            // channels past the row's end hold the pivot and add nothing
-            const uint32_t fill_w = pack_bf16x2(q, q);
-            if (LAYER) q = bf16lo(fill_w);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const int u = t + TPR * j;
                 if (u < NU) {
-                    h[j] = reinterpret_cast<const Packed<U>*>(at + x_bytes)[u];
+                    load_res(at, u, y[j]);
+                    if (has_h) h[j] = reinterpret_cast<const Packed<U>*>(at + x_bytes)[u];
                 } else {
+#pragma unroll
+                    for (int i = 0; i < P; ++i) y[j][i] = both(p);
                     if constexpr (U == 8)
-                        h[j] = make_uint4(fill_w, fill_w, fill_w, fill_w);
+                        h[j] = make_uint4(q_word, q_word, q_word, q_word);
                     else
-                        h[j] = make_uint2(fill_w, fill_w);
+                        h[j] = make_uint2(q_word, q_word);
                 }
             }
-            float r, mean_h = 0.0f;
-            if constexpr (!LAYER) {
-                float2 s2 = both(0.0f);
-#pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    float2 f[P];
-                    unpack(h[j], f);
-#pragma unroll
-                    for (int i = 0; i < P; ++i) s2 = __ffma2_rn(f[i], f[i], s2);
-                }
-                float s[1] = {s2.x + s2.y};
-                team.sum(s);
-                r = rsqrtf(__fmaf_rn(s[0], inv_c, a.eps));
-            } else {
-                float off = q;
-                for (int again = 0;; ++again) {
-                    // sums about the pivot; those of x and A (h - pivot) lead to y's mean
-                    float2 s1 = both(0.0f), s2 = both(0.0f), sx = both(0.0f), sa = both(0.0f);
-                    const float2 o2 = both(-off);
+            // a row that never came (its wait ran out) must not pass for one
+            if (!ok) y[0][0].x = __int_as_float(0x7FC00000);
+            if (has_h) {
+                float r, mean_h = 0.0f;
+                if constexpr (!LAYER) {
+                    float2 s2 = both(0.0f);
 #pragma unroll
                     for (int j = 0; j < J; ++j) {
                         float2 f[P];
                         unpack(h[j], f);
 #pragma unroll
-                        for (int i = 0; i < P; ++i) {
-                            f[i] = __fadd2_rn(f[i], o2);
-                            if (again && t + TPR * j >= NU) f[i] = both(0.0f);
-                            s1 = __fadd2_rn(s1, f[i]);
-                            s2 = __ffma2_rn(f[i], f[i], s2);
-                            sa = __ffma2_rn(f[i], A[j][i], sa);
-                            sx = __fadd2_rn(sx, y[j][i]);
-                        }
+                        for (int i = 0; i < P; ++i) s2 = __ffma2_rn(f[i], f[i], s2);
                     }
-                    float s[4] = {s1.x + s1.y, s2.x + s2.y, sa.x + sa.y, sx.x + sx.y};
+                    float s[1] = {s2.x + s2.y};
                     team.sum(s);
-                    const float d = s[0] * inv_c, var = __fmaf_rn(-d, d, s[1] * inv_c);
-                    mean_h = off + d;
+                    r = rsqrtf(__fmaf_rn(s[0], inv_c, a.eps));
+                } else {
+                    auto moments = [&](float pivot, bool all, float& d) {
+                        float2 s1 = both(0.0f), s2 = both(0.0f);
+#pragma unroll
+                        for (int j = 0; j < J; ++j) {
+                            float2 f[P];
+                            unpack(h[j], f);
+                            if (all || t + TPR * j < NU)
+#pragma unroll
+                                for (int i = 0; i < P; ++i) {
+                                    f[i] = __fadd2_rn(f[i], both(-pivot));
+                                    s1 = __fadd2_rn(s1, f[i]);
+                                    s2 = __ffma2_rn(f[i], f[i], s2);
+                                }
+                        }
+                        float s[2] = {s1.x + s1.y, s2.x + s2.y};
+                        team.sum(s);
+                        d = s[0] * inv_c;
+                        return __fmaf_rn(-d, d, s[1] * inv_c);
+                    };
+                    float d, var = moments(q, true, d);
+                    mean_h = q + d;
+                    if (!(d * d <= var)) {
+                        var = moments(mean_h, false, d);
+                        mean_h += d;
+                    }
                     r = rsqrtf(fmaxf(var, 0.0f) + a.eps);
-                    mean = s[3] * inv_c + r * (s[2] * inv_c - d * mean_A);
-                    if (again || d * d <= var) break;
-                    off = mean_h;
+                }
+                // (h - mean) r as h r - mean r: its rounding is of the size of the mean's own
+                const float2 r2 = both(r), mr2 = both(-mean_h * r);
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    if (t + TPR * j < NU) {
+                        float2 f[P], A[P];
+                        unpack(h[j], f);
+                        vector(0, t + TPR * j, A);
+#pragma unroll
+                        for (int i = 0; i < P; ++i)
+                            y[j][i] = __ffma2_rn(A[i], LAYER ? __ffma2_rn(f[i], r2, mr2) : __fmul2_rn(f[i], r2), y[j][i]);
+                    }
+                }
+            } else {
+                team.sync();
+            }
+            // every thread has its row: the slot is free
+            if (t == 0 && next < r1 && !*abort_flag) fill(slot);
+            if (++slot == a.slots) {
+                slot = 0;
+                parity ^= 1;
+            }
+            if (a.y) {
+                void* y_at = static_cast<uint8_t*>(a.y) + (row * a.ldy + c0) * ES;
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const int u = t + TPR * j;
+                    if (u < NU && FP4ATTN_IN_BOUNDS(row < a.rows && c0 + U * u + U <= a.C, a.status)) store_res(y_at, u, y[j]);
                 }
             }
-            const float2 m2 = both(-mean_h), r2 = both(r);
+            if (!QUANT && !a.z) continue;
+            float r, mr = 0.0f;  // norm(y) = y r + mr
+            if constexpr (!LAYER) {
+                float2 s2 = both(0.0f);
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                float2 f[P];
-                unpack(h[j], f);
+                for (int j = 0; j < J; ++j)
 #pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    if (LAYER) f[i] = __fadd2_rn(f[i], m2);
-                    y[j][i] = __ffma2_rn(A[j][i], __fmul2_rn(f[i], r2), y[j][i]);
+                    for (int i = 0; i < P; ++i) s2 = __ffma2_rn(y[j][i], y[j][i], s2);
+                float s[1] = {s2.x + s2.y};
+                team.sum(s);
+                r = rsqrtf(__fmaf_rn(s[0], inv_c, a.eps));
+            } else {
+                auto moments = [&](float pivot, bool all, float& d) {
+                    float2 s1 = both(0.0f), s2 = both(0.0f);
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+                        if (all || t + TPR * j < NU)
+#pragma unroll
+                            for (int i = 0; i < P; ++i) {
+                                const float2 f = __fadd2_rn(y[j][i], both(-pivot));
+                                s1 = __fadd2_rn(s1, f);
+                                s2 = __ffma2_rn(f, f, s2);
+                            }
+                    float s[2] = {s1.x + s1.y, s2.x + s2.y};
+                    team.sum(s);
+                    d = s[0] * inv_c;
+                    return __fmaf_rn(-d, d, s[1] * inv_c);
+                };
+                float d, var = moments(p, true, d);
+                p += d;
+                if (!(d * d <= var)) {
+                    var = moments(p, false, d);
+                    p += d;
                 }
+                r = rsqrtf(fmaxf(var, 0.0f) + a.eps);
+                mr = -p * r;
             }
-        } else if (LAYER) {
-            float s[1] = {0.0f};
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-#pragma unroll
-                for (int i = 0; i < P; ++i) s[0] += y[j][i].x + y[j][i].y;
-            team.sum(s);
-            mean = s[0] * inv_c;
-        } else {
-            team.sync();
-        }
-        // every thread has its row: the slot is free
-        if (t == 0 && next < r1 && !*abort_flag) {
-            fill(slot);
-            ++next;
-        }
-        if (++slot == a.slots) {
-            slot = 0;
-            parity ^= 1;
-        }
-        if (a.y) {
+            __nv_bfloat16* z_at = a.z + (row * a.ldz + c0);
+            uint8_t* codes_at = a.codes + (row * a.C + c0) / 2;
+            // where the scales of this row's first chunk go; a chunk is 128 words on
+            uint32_t* scales_at = reinterpret_cast<uint32_t*>(a.scales) + ((row >> 7) * a.chunks + c0 / 64) * 128 +
+                                  scale_word_in_tile((uint32_t)row & 127);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const int u = t + TPR * j;
-                if (u < NU && FP4ATTN_IN_BOUNDS(row < a.rows && c0 + U * u + U <= a.C, a.status)) store_res(y_at, u, y[j]);
-            }
-        }
-        if (!QUANT && !a.z) continue;
-        float2 s1 = both(0.0f), s2 = both(0.0f);
+                float2 z[P];
+                if (u < NU) {
+                    float2 B[P], S[P];
+                    vector(1, u, B);
+                    vector(2, u, S);
 #pragma unroll
-        for (int j = 0; j < J; ++j)
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                if constexpr (LAYER) {
-                    y[j][i] = t + TPR * j < NU ? __fadd2_rn(y[j][i], both(-mean)) : both(0.0f);
-                    s1 = __fadd2_rn(s1, y[j][i]);
-                }
-                s2 = __ffma2_rn(y[j][i], y[j][i], s2);
-            }
-        float d = 0.0f, r;
-        if constexpr (LAYER) {
-            float s[2] = {s1.x + s1.y, s2.x + s2.y};
-            team.sum(s);
-            d = s[0] * inv_c;
-            r = rsqrtf(fmaxf(__fmaf_rn(-d, d, s[1] * inv_c), 0.0f) + a.eps);
-        } else {
-            float s[1] = {s2.x + s2.y};
-            team.sum(s);
-            r = rsqrtf(__fmaf_rn(s[0], inv_c, a.eps));
-        }
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int u = t + TPR * j;
-            float2 z[P];
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const float2 n = LAYER ? __fadd2_rn(y[j][i], both(-d)) : y[j][i];
-                z[i] = __ffma2_rn(__fmul2_rn(n, both(r)), B[j][i], S[j][i]);
-            }
-            const Packed<U> w = pack(z);
-            if constexpr (!QUANT) {
-                if (u < NU && FP4ATTN_IN_BOUNDS(row < a.rows && c0 + U * u + U <= a.C, a.status))
-                    reinterpret_cast<Packed<U>*>(z_at)[u] = w;
-            } else {
-                // 16 / U lanes share a block, 64 / U a word of four scales
-                unpack(w, z);
-                float m = 0.0f;
-#pragma unroll
-                for (int i = 0; i < P; ++i) m = max_nan(m, max_nan(fabsf(z[i].x), fabsf(z[i].y)));
-                if (u >= NU) m = 0.0f;
-#pragma unroll
-                for (int o = 1; o < 16 / U; o *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-                finite = finite && (m < INFINITY);
-                uint32_t s8;
-                float inv;
-                row_block_scale(m, gz, s8, inv);
-#pragma unroll
-                for (int i = 0; i < P; ++i) z[i] = __fmul2_rn(z[i], both(inv));
-                const bool on = u < NU && FP4ATTN_IN_BOUNDS(row < a.rows && c0 + U * u + U <= a.C, a.status);
-                uint8_t* codes = a.codes + row * (a.C / 2) + (c0 + U * u) / 2;
-                if constexpr (U == 8) {
-                    const uint32_t c = cvt_e2m1x8(z[0].x, z[0].y, z[1].x, z[1].y, z[2].x, z[2].y, z[3].x, z[3].y);
-                    if (on) *reinterpret_cast<uint32_t*>(codes) = c;
+                    for (int i = 0; i < P; ++i)
+                        z[i] = __ffma2_rn(
+                            LAYER ? __ffma2_rn(y[j][i], both(r), both(mr)) : __fmul2_rn(y[j][i], both(r)), B[i], S[i]);
                 } else {
-                    const uint32_t c = cvt_e2m1x8(z[0].x, z[0].y, z[1].x, z[1].y, 0.0f, 0.0f, 0.0f, 0.0f);
-                    if (on) *reinterpret_cast<uint16_t*>(codes) = (uint16_t)c;
-                }
-                uint32_t word = s8 << (8 * ((u * U / 16) & 3));
 #pragma unroll
-                for (int o = 16 / U; o < 64 / U; o *= 2) word |= __shfl_xor_sync(0xffffffffu, word, o);
-                const int64_t off =
-                    ((row >> 7) * a.chunks + (c0 + U * u) / 64) * 128 + scale_word_in_tile((uint32_t)row & 127);
-                if (on && u % (64 / U) == 0 && FP4ATTN_IN_BOUNDS(4 * off + 4 <= scale_tile_bytes(a.rows, a.C), a.status))
-                    reinterpret_cast<uint32_t*>(a.scales)[off] = word;
+                    for (int i = 0; i < P; ++i) z[i] = both(0.0f);
+                }
+                const Packed<U> w = pack(z);
+                const bool on = u < NU && FP4ATTN_IN_BOUNDS(row < a.rows && c0 + U * u + U <= a.C, a.status);
+                if constexpr (!QUANT) {
+                    if (on) reinterpret_cast<Packed<U>*>(z_at)[u] = w;
+                } else {
+                    // 16 / U lanes share a block, 64 / U a word of four scales
+                    unpack(w, z);
+                    uint32_t m2 = amax_pair(w);
+#pragma unroll
+                    for (int o = 1; o < 16 / U; o *= 2) m2 = max_pair(m2, __shfl_xor_sync(0xffffffffu, m2, o));
+                    const float m = max_nan(bf16lo(m2), bf16hi(m2));
+                    finite = finite && (m < INFINITY);
+                    uint32_t s8;
+                    float inv;
+                    row_block_scale(table, guess, m, gz, s8, inv);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) z[i] = __fmul2_rn(z[i], both(inv));
+                    if constexpr (U == 8) {
+                        const uint32_t c = cvt_e2m1x8(z[0].x, z[0].y, z[1].x, z[1].y, z[2].x, z[2].y, z[3].x, z[3].y);
+                        if (on) reinterpret_cast<uint32_t*>(codes_at)[u] = c;
+                    } else {
+                        const uint32_t c = cvt_e2m1x8(z[0].x, z[0].y, z[1].x, z[1].y, 0.0f, 0.0f, 0.0f, 0.0f);
+                        if (on) reinterpret_cast<uint16_t*>(codes_at)[u] = (uint16_t)c;
+                    }
+                    uint32_t word = s8 << sf_shift;
+#pragma unroll
+                    for (int o = 16 / U; o < 64 / U; o *= 2) word |= __shfl_xor_sync(0xffffffffu, word, o);
+                    if (on && t % (64 / U) == 0 &&
+                        FP4ATTN_IN_BOUNDS(((row >> 7) * a.chunks + (c0 + U * u) / 64) * 512 + 512 <= scale_tile_bytes(a.rows, a.C),
+                                          a.status))
+                        scales_at[U * u / 64 * 128] = word;
+                }
             }
         }
     }
@@ -566,8 +605,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) norm_gate_bwd_kernel(const __grid
             Packed<U> dz[J], h[J];
             float p = 0.0f, q = 0.0f;
             if (LAYER) {
-                p = pivot_of<U>(at, cols);
-                if (has_h) q = pivot_of<8>(at + at_h, cols);
+                p = pivot_of<U>(at, NU);
+                if (has_h) q = pivot_of<U == 8 ? 8 : 2>(at + at_h, NU);
                 share_pivots(team, p, q);
             }
 #pragma unroll
@@ -805,6 +844,7 @@ __global__ void __launch_bounds__(256) norm_weights_kernel(const __grid_constant
     if (a.dpost) a.dpost[c] = s[1];
 }
 
+// Shared memory of the rings (and the forward's vectors).
 constexpr size_t RING_BYTES = 222 * 1024;
 // the backward fills a slot one row late: it needs two at its widest rows
 static_assert(2 * 12 * (size_t)NTHREADS * MAX_VALUES <= RING_BYTES, "two slots of the widest rows");
@@ -833,11 +873,10 @@ struct Shape {
     int slots;
     size_t smem;
 };
-int shape_of(const void* kernel, const Split& s, size_t slot_bytes, int64_t work, Shape& sh) {
-    const int teams = NTHREADS / s.tpr;
-    sh.slots = (int)(RING_BYTES / (slot_bytes * teams));
+int shape_of(const void* kernel, const Split& s, int teams, size_t fixed_bytes, size_t slot_bytes, int64_t work, Shape& sh) {
+    sh.slots = (int)((RING_BYTES - fixed_bytes) / (slot_bytes * teams));
     sh.slots = sh.slots < 1 ? 1 : sh.slots > MAX_SLOTS ? MAX_SLOTS : sh.slots;
-    sh.smem = slot_bytes * teams * sh.slots;
+    sh.smem = fixed_bytes + slot_bytes * teams * sh.slots;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
@@ -850,10 +889,10 @@ int shape_of(const void* kernel, const Split& s, size_t slot_bytes, int64_t work
 }
 
 template <typename Args>
-int launch(void (*kernel)(Args), const Args& a, const Split& s, const Shape& sh, cudaStream_t stream) {
+int launch(void (*kernel)(Args), const Args& a, int threads, const Split& s, const Shape& sh, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(sh.grid);
-    cfg.blockDim = dim3(NTHREADS);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = sh.smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -906,10 +945,11 @@ int launch_norm_gate(const NormArgs& a0, bool f32, cudaStream_t stream) {
     a.cols = s.cols;
     a.slot_bytes = (uint32_t)s.cols * ((f32 ? 4 : 2) + (a.h ? 2 : 0));
     Shape sh;
-    const int st = shape_of(reinterpret_cast<const void*>(kernel), s, a.slot_bytes, a.rows, sh);
+    const int st = shape_of(reinterpret_cast<const void*>(kernel), s, s.ctas > 1 ? 1 : FWD_THREADS / s.tpr, (size_t)12 * s.cols,
+                            a.slot_bytes, a.rows, sh);
     if (st != FP4ATTN_OK) return st;
     a.slots = sh.slots;
-    return launch(kernel, a, s, sh, stream);
+    return launch(kernel, a, s.ctas > 1 ? s.tpr : FWD_THREADS, s, sh, stream);
 }
 
 // Parts of a sample's rows: the longest work of a team, ceil(groups * parts /
@@ -938,10 +978,10 @@ int launch_norm_gate_backward(const NormBwdArgs& a0, bool f32, cudaStream_t stre
     a.cols = s.cols;
     a.slot_bytes = (uint32_t)s.cols * ((f32 ? 4 : 2) * (a.dy ? 2 : 1) + (a.h ? 4 : 2));
     Shape sh;
-    const int st = shape_of(reinterpret_cast<const void*>(kernel), s, a.slot_bytes, a.groups * a.parts, sh);
+    const int st = shape_of(reinterpret_cast<const void*>(kernel), s, NTHREADS / s.tpr, 0, a.slot_bytes, a.groups * a.parts, sh);
     if (st != FP4ATTN_OK) return st;
     a.slots = sh.slots;
-    if (launch(kernel, a, s, sh, stream) != FP4ATTN_OK) return FP4ATTN_ERR_CUDA;
+    if (launch(kernel, a, NTHREADS, s, sh, stream) != FP4ATTN_OK) return FP4ATTN_ERR_CUDA;
     const int64_t blocks = (a.C + 31) / 32;
     norm_join_kernel<<<(unsigned)(blocks * a.groups), 256, 0, stream>>>(a);
     if (cudaGetLastError() != cudaSuccess) return FP4ATTN_ERR_CUDA;

@@ -42,6 +42,60 @@ __device__ __forceinline__ void row_block_scale(float a, float g, uint32_t& s, f
     inv = (sd != 0.0f) ? __frcp_rn(__fmul_rn(g, sd)) : 0.0f;
 }
 
+// The same for many blocks under one g, from two small tables: the scale of a
+// block is a non-decreasing function F of its largest magnitude a, so a guess
+// within one step (a times 1 / (6 g), rounded to E4M3) is put right by
+// comparing a with the smallest values that reach the guess and the step above
+// it.  No divide, and the same bits: the table is made with the definition.
+//   least[c]  smallest a whose scale byte is at least c (c = 1..126); 0 and
+//             infinity at the ends
+//   recip[c]  fl(1 / fl(g s)), 0 for c = 0
+struct ScaleTable {
+    float least[129];
+    float recip[128];
+    float guess;  // 1 / (6 g); 0: g is out of the range where the guess holds
+};
+
+// Made by the first 128 threads of a block; the caller synchronises behind it.
+__device__ __forceinline__ void make_scale_table(ScaleTable& tab, float g, int t) {
+    if (t >= 128) return;
+    // beyond these, fl(a / 6) or the guess could be subnormal or overflow where the scale is neither 0 nor 448
+    const bool usable = g > 7.888609052210118e-31f && g < 1.2676506002282294e30f;  // 2^-100, 2^100
+    const float sd = ue4m3_value((uint32_t)t);
+    tab.recip[t] = t ? __frcp_rn(__fmul_rn(g, sd)) : 0.0f;
+    if (t == 0) tab.guess = usable ? __frcp_rn(6.0f * g) : 0.0f;
+    if (t == 0) tab.least[0] = 0.0f;
+    if (t == 127) tab.least[127] = tab.least[128] = INFINITY;
+    if (t == 0 || t == 127 || !usable) return;
+    auto reaches = [&](float a) {
+        float q = div6_rn(a);
+        if (g != 1.0f) q = __fdiv_rn(q, g);
+        return (cvt_e4m3(q) & 0x7Fu) >= (uint32_t)t;
+    };
+    // start at the border between the two scales and walk to the exact value (a
+    // few units in the last place; bounded in any case)
+    float a = 6.0f * g * (0.5f * (sd + ue4m3_value((uint32_t)t - 1)));
+    for (int i = 0; i < 16 && !reaches(a); ++i) a = __int_as_float(__float_as_int(a) + 1);
+    for (int i = 0; i < 16 && reaches(__int_as_float(__float_as_int(a) - 1)); ++i) a = __int_as_float(__float_as_int(a) - 1);
+    tab.least[t] = a;
+}
+
+__device__ __forceinline__ void row_block_scale(const ScaleTable& tab, float guess, float a, float g, uint32_t& s,
+                                                float& inv) {
+    if (guess != 0.0f) {
+        uint32_t c = cvt_e4m3(a * guess) & 0x7Fu;
+        c = c > 126u ? 126u : c;
+        const float lo = tab.least[c], hi = tab.least[c + 1];
+        c = a < lo ? c - 1u : c;
+        c = a >= hi ? c + 1u : c;
+        c = c > 126u ? 126u : c;  // an infinite a
+        s = c;
+        inv = tab.recip[c];
+    } else {
+        row_block_scale(a, g, s, inv);
+    }
+}
+
 // Codes of eight values times inv.
 __device__ __forceinline__ uint32_t row_codes8(const float (&v)[8], float inv) {
     const float2 i2 = make_float2(inv, inv);
