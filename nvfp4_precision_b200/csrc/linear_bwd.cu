@@ -22,6 +22,7 @@
 #include <cuda_bf16.h>
 
 #include "nvfp4_rows.cuh"
+#include "tile_store.cuh"
 
 namespace fp4attn {
 
@@ -29,8 +30,8 @@ namespace {
 
 constexpr int BM = 256;  // rows of a pair's tile
 constexpr int BKC = 64;  // contraction per stage
-constexpr int THREADS = 192;
-constexpr int WARP_PRODUCER = 4, WARP_MMA = 5;
+constexpr int THREADS = 32 * (STORE_WARPS + 2);
+constexpr int WARP_PRODUCER = STORE_WARPS, WARP_MMA = STORE_WARPS + 1;
 constexpr uint32_t PANEL = 64 * 128;  // 64 rows of 64 bf16
 constexpr uint64_t kLimitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
@@ -41,7 +42,7 @@ struct Cfg {
     static constexpr uint32_t A_BYTES = 2 * PANEL;               // 128 rows (or columns) of A per CTA
     static constexpr uint32_t B_BYTES = (TN / 128) * PANEL;      // TN / 2 columns of B per CTA
     static constexpr uint32_t STAGE = A_BYTES + B_BYTES;
-    static constexpr int STAGES = (int)(200u * 1024 / STAGE) < 8 ? (int)(200u * 1024 / STAGE) : 8;
+    static constexpr int STAGES = (int)(193u * 1024 / STAGE) < 8 ? (int)(193u * 1024 / STAGE) : 8;
 };
 
 struct Bars {
@@ -112,7 +113,8 @@ __device__ __forceinline__ Unit unit_of(const BwdGemmParams& p, int u) {
 template <int TN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     linear_bwd_kernel(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_w,
-                      const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ BwdGemmParams p) {
+                      const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_out0,
+                      const __grid_constant__ CUtensorMap tm_out1, const __grid_constant__ BwdGemmParams p) {
     using C = Cfg<TN>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars sm;
@@ -130,7 +132,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sm.acc_full[i]), 1);
-            mbar_init(smem_u32(&sm.acc_empty[i]), 8);  // four epilogue warps of either CTA
+            mbar_init(smem_u32(&sm.acc_empty[i]), 2 * STORE_WARPS);  // the epilogue warps of both CTAs
         }
         mbar_init(smem_u32(&sm.final_), 1);
         sm.abort_flag = 0;
@@ -241,8 +243,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
     } else {
         // ------------------------------------------------------ epilogue --
-        const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-        const int in_tile = 128 * (int)rank + 32 * warp + lane;
+        // a warp reads its quarter of the lanes and half of the columns, 64 at a time
+        const int quarter = warp & 3, half = warp >> 2;
+        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+        const uint32_t box = ring_u + C::STAGES * C::STAGE + STORE_BOX * warp;
         int local = 0;
         for (int u = pair; u < units; u += pairs, ++local) {
             const Unit w = unit_of(p, u);
@@ -255,40 +259,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 const float g1 = p.prod[1].g ? __ldg(p.prod[1].g) : 1.0f;
                 if (bad_gscale(g) || bad_gscale(g1)) raise_status(p.status, FP4ATTN_ERR_RANGE);
             }
-            const int row = BM * w.rt + in_tile;
+            const int row0 = BM * w.rt + 128 * (int)rank + 32 * quarter, row = row0 + lane;
 #pragma unroll 1
-            for (int c0 = 0; c0 < TN; c0 += 32) {
-                uint32_t r[32];
-                tmem_ld32(acc + c0, r);
+            for (int i = 0; i < TN / 128; ++i) {
+                const int c0 = TN / 2 * half + 64 * i, col = TN * w.ct + c0;
+                uint32_t r[2][32];
+                tmem_ld32(acc + c0, r[0]);
+                tmem_ld32(acc + c0 + 32, r[1]);
                 tmem_wait_ld();
-                if (c0 + 32 == TN) {
+                if (i == TN / 128 - 1) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&sm.acc_empty[local & 1]), 0));
                 }
-                const int col = TN * w.ct + c0;  // K is a multiple of 32
-                if (row < q.rows && col < p.K && FP4ATTN_IN_BOUNDS(w.part < q.split && col + 32 <= p.K, p.status)) {
-                    if (q.split > 1) {
-                        float4* dst = reinterpret_cast<float4*>(q.part + ((long long)w.part * q.rows + row) * p.K + col);
+                if (q.split > 1) {
+                    // K is a multiple of 32
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            dst[i] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
-                                                 __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
-                    } else {
-                        float v[32];
+                    for (int h = 0; h < 2; ++h)
+                        if (row < q.rows && col + 32 * h < p.K && FP4ATTN_IN_BOUNDS(w.part < q.split, p.status)) {
+                            float4* dst =
+                                reinterpret_cast<float4*>(q.part + ((long long)w.part * q.rows + row) * p.K + col + 32 * h);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = g * __uint_as_float(r[i]);
-                        uint4* dst = reinterpret_cast<uint4*>(q.out + (long long)row * q.ld + col);
+                            for (int k = 0; k < 8; ++k)
+                                dst[k] = make_float4(__uint_as_float(r[h][4 * k]), __uint_as_float(r[h][4 * k + 1]),
+                                                     __uint_as_float(r[h][4 * k + 2]), __uint_as_float(r[h][4 * k + 3]));
+                        }
+                } else {
+                    uint32_t v[32];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            dst[i] = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                                                pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
-                                                pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
-                    }
+                    for (int k = 0; k < 32; ++k)
+                        v[k] = pack_bf16x2(__uint_as_float(r[k / 16][2 * (k % 16)]) * g,
+                                           __uint_as_float(r[k / 16][2 * (k % 16) + 1]) * g);
+                    store_box(w.which ? &tm_out1 : &tm_out0, box, v, row0, col, q.rows, p.K, lane);
                 }
                 __syncwarp();
             }
         }
+        store_box_finish(lane);
     }
     tc_fence_before();
     __syncthreads();
@@ -388,14 +395,15 @@ int64_t part_floats(const Plan& pl, int64_t M, int64_t N, int64_t K, bool want_d
 }
 
 template <int TN>
-int launch_products(const BwdGemmParams& p, const CUtensorMap& dy, const CUtensorMap& w, const CUtensorMap& x, int pairs,
-                    cudaStream_t stream) {
+int launch_products(const BwdGemmParams& p, const CUtensorMap& dy, const CUtensorMap& w, const CUtensorMap& x,
+                    const CUtensorMap (&out)[2], int pairs, cudaStream_t stream) {
     using C = Cfg<TN>;
-    constexpr size_t smem = (size_t)C::STAGE * C::STAGES + 1024;
+    constexpr size_t smem = (size_t)C::STAGE * C::STAGES + STORE_BYTES + 1024;
+    static_assert(smem + sizeof(Bars) <= 227 * 1024, "shared memory budget");
     auto kernel = linear_bwd_kernel<TN>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return FP4ATTN_ERR_CUDA;
-    kernel<<<2 * pairs, THREADS, smem, stream>>>(dy, w, x, p);
+    kernel<<<2 * pairs, THREADS, smem, stream>>>(dy, w, x, out[0], out[1], p);
     return cudaGetLastError() == cudaSuccess ? FP4ATTN_OK : FP4ATTN_ERR_CUDA;
 }
 
@@ -458,10 +466,14 @@ int launch_linear_backward(const LinearBwdArgs& a, cudaStream_t stream) {
     w = x = dy;
     if (a.dx && !make_map(&w, a.w_bf16, a.N, a.K, a.K)) return FP4ATTN_ERR_CUDA;
     if (a.dw && !make_map(&x, a.x_bf16, a.M, a.K, a.K)) return FP4ATTN_ERR_CUDA;
+    CUtensorMap out[2] = {dy, dy};  // a split product, or an absent one, does not use its own
+    for (int i = 0; i < 2; ++i)
+        if (p.prod[i].units && !make_store_map(&out[i], p.prod[i].out, p.prod[i].rows, a.K, p.prod[i].ld))
+            return FP4ATTN_ERR_CUDA;
     const int units = p.prod[0].units + p.prod[1].units;
     const int pairs = units < sms / 2 ? units : sms / 2;
-    const int st = pl.tn == 256 ? launch_products<256>(p, dy, w, x, pairs, stream)
-                                : launch_products<128>(p, dy, w, x, pairs, stream);
+    const int st = pl.tn == 256 ? launch_products<256>(p, dy, w, x, out, pairs, stream)
+                                : launch_products<128>(p, dy, w, x, out, pairs, stream);
     if (st != FP4ATTN_OK) return st;
     if (p.prod[0].split > 1 || p.prod[1].split > 1) {
         long long n = 0;
