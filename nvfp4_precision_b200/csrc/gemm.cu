@@ -79,7 +79,7 @@ struct GemmParams {
     __nv_bfloat16* out;
     long long ld;
     int N;
-    int pdl;
+    int weight_ready;  // the weight may be loaded before the kernel in front has finished
     int* status;
 };
 
@@ -172,10 +172,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (warp == WARP_PRODUCER) {
         // ------------------------------------------------------ producer --
-        // One operand is x, which the launch before may still be writing: the
-        // first stages of the weight go out before that launch is waited for.
+        // x may still be written by the launch in front: where the weight is not
+        // (the linear layer's own quantiser), its first stages go out before that
+        // launch is waited for.
         int it = 0;
-        bool waited = p.pdl == 0;
+        bool waited = p.weight_ready == 0;
+        if (waited) pdl_wait();
         auto copy_p = [&](int slot, int ks, int pt) {
             const uint32_t full = smem_u32(&sm.full[slot]);
             const uint32_t at = ring_u + C::STAGE * slot;
@@ -216,7 +218,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         copy_p(i, ks + i, pt);
                     }
                 }
-                asm volatile("griddepcontrol.wait;" ::: "memory");
+                pdl_wait();
                 if (lane == 0) {
                     for (int i = 0; i < pre; ++i) copy_q(i, ks + i, qt);
                 }
@@ -240,7 +242,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
             }
         }
-        if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (!waited) pdl_wait();
         if (lane == 0 && *abort_flag) {
             // wind down: this CTA's own copies land before it exits
             for (int i = (it > C::STAGES ? it - C::STAGES : 0); i < it; ++i)
@@ -301,7 +303,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
     } else {
         // ------------------------------------------------------ epilogue --
-        if (p.pdl) asm volatile("griddepcontrol.wait;" ::: "memory");
+        pdl_wait();
+        pdl_trigger();
         const float gx = p.gx ? __ldcg(p.gx) : 1.0f, gw = p.gw ? __ldg(p.gw) : 1.0f;
         if (blockIdx.x == 0 && threadIdx.x == 0 && (bad_gscale(gx) || bad_gscale(gw)))
             raise_status(p.status, FP4ATTN_ERR_RANGE);
@@ -466,7 +469,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
     volatile int* abort_flag = &sm.abort_flag;
-    if (p.pdl) asm volatile("griddepcontrol.wait;" ::: "memory");
+    pdl_wait();
+    pdl_trigger();
 
     if (warp == PAIR_PRODUCER) {
         // ------------------------------------------------------ producer --
@@ -666,27 +670,10 @@ int launch_one(const GemmFp4Args& a, GemmParams& p, int split, int sms, cudaStre
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return FP4ATTN_ERR_CUDA;
     const long long tiles = (long long)p.p_tiles * p.q_tiles;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * split : (tiles < sms ? tiles : sms)));
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    int n = 0;
-    if (SPLIT) {
-        attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = (unsigned)split;
-        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
-        ++n;
-    }
-    if (p.pdl) {
-        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[n].val.programmaticStreamSerializationAllowed = 1;
-        ++n;
-    }
-    cfg.attrs = attr;
-    cfg.numAttrs = (unsigned)n;
-    return cudaLaunchKernelEx(&cfg, kernel, tp, tq, p) == cudaSuccess ? FP4ATTN_OK : FP4ATTN_ERR_CUDA;
+    const unsigned grid = (unsigned)(SPLIT ? tiles * split : (tiles < sms ? tiles : sms));
+    return launch_behind(kernel, dim3(grid), THREADS, smem, stream, SPLIT ? split : 1, tp, tq, p) == cudaSuccess
+               ? FP4ATTN_OK
+               : FP4ATTN_ERR_CUDA;
 }
 
 template <bool SWAP>
@@ -710,19 +697,10 @@ int launch_pair(const GemmFp4Args& a, GemmParams& p, int sms, cudaStream_t strea
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return FP4ATTN_ERR_CUDA;
     const long long tiles = (long long)p.p_tiles * p.q_tiles, pairs = sms / 2;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
-    cfg.blockDim = dim3(PAIR_THREADS);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    if (p.pdl) {
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-    }
-    return cudaLaunchKernelEx(&cfg, kernel, tp, tq, tsp, tsq, to, p) == cudaSuccess ? FP4ATTN_OK : FP4ATTN_ERR_CUDA;
+    return launch_behind(kernel, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), PAIR_THREADS, smem, stream, 1, tp, tq,
+                         tsp, tsq, to, p) == cudaSuccess
+               ? FP4ATTN_OK
+               : FP4ATTN_ERR_CUDA;
 }
 
 }  // namespace
@@ -742,7 +720,7 @@ int launch_gemm_fp4(const GemmFp4Args& a, cudaStream_t stream) {
     p.out = a.out;
     p.ld = a.ld;
     p.N = (int)a.N;
-    p.pdl = a.after_quantize ? 1 : 0;
+    p.weight_ready = a.weight_ready ? 1 : 0;
     p.status = a.status;
     // Tiles of 128 x 128.  More than one a SM: pairs, with x on the lanes where the
     // output's rows take bulk stores.  2048 x 2048 x 6144 (256 tiles): 15.3 us in

@@ -200,7 +200,6 @@ struct QuantRowsArgs {
     const float* g;  // device scalar or nullptr (1.0); ignored when dynamic
     float* g_out;    // dynamic: receives the computed g
     bool dynamic;
-    bool pdl;        // let the launch behind this one start early
     float* part;     // dynamic: ROWS_AMAX_PARTS floats
     int n_part;      // set by the launcher
     uint8_t* codes;  // [rows][K/2]
@@ -226,7 +225,7 @@ struct GemmFp4Args {
     int64_t M, N, K;
     __nv_bfloat16* out;
     int64_t ld;
-    bool after_quantize;  // launched right behind the kernel that writes x: may start before it ends
+    bool weight_ready;  // the kernel in front writes x only: the weight may be loaded before it has finished
     int* status;
 };
 int launch_gemm_fp4(const GemmFp4Args& a, cudaStream_t stream);

@@ -13,7 +13,7 @@ namespace {
 
 constexpr int64_t kMaxRows = 4194304;  // 2^22: tile counts and coordinates stay far inside 32 bits
 constexpr int64_t kMaxK = 1048576;
-constexpr int64_t kMaxStride = (int64_t)1 << 39;
+constexpr int64_t kMaxStride = (int64_t)1 << 38;  // bytes stay below what tensor maps hold
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -194,7 +194,6 @@ int fp4attn_linear(const void* x, int64_t x_stride, float* gx, uint32_t flags, c
     q.g = dynamic ? nullptr : g;
     q.g_out = dynamic ? g : nullptr;
     q.dynamic = dynamic;
-    q.pdl = true;
     q.part = reinterpret_cast<float*>(ws + lws_part_offset());
     q.codes = ws + lws_codes_offset();
     q.scales = q.codes + round256((size_t)(M * (K / 2)));
@@ -214,7 +213,7 @@ int fp4attn_linear(const void* x, int64_t x_stride, float* gx, uint32_t flags, c
     a.K = K;
     a.out = static_cast<__nv_bfloat16*>(y);
     a.ld = M > 1 ? y_stride : N;
-    a.after_quantize = true;
+    a.weight_ready = true;
     a.status = q.status;
     return clear_error(launch_gemm_fp4(a, stream));
 }

@@ -153,6 +153,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
     volatile int* abort_flag = &sm.abort_flag;
+    pdl_wait();
+    pdl_trigger();
 
     if (warp == WARP_PRODUCER) {
         // ------------------------------------------------------ producer --
@@ -308,6 +310,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
 // out = g * (sum of the parts, in order), eight columns per thread.
 __global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ BwdGemmParams p) {
+    pdl_wait();
+    pdl_trigger();
     const long long per_row = p.K / 8;
     const long long n0 = p.prod[0].split > 1 ? p.prod[0].rows * per_row : 0;
     const long long n1 = p.prod[1].split > 1 ? p.prod[1].rows * per_row : 0;
@@ -403,8 +407,9 @@ int launch_products(const BwdGemmParams& p, const CUtensorMap& dy, const CUtenso
     auto kernel = linear_bwd_kernel<TN>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return FP4ATTN_ERR_CUDA;
-    kernel<<<2 * pairs, THREADS, smem, stream>>>(dy, w, x, out[0], out[1], p);
-    return cudaGetLastError() == cudaSuccess ? FP4ATTN_OK : FP4ATTN_ERR_CUDA;
+    return launch_behind(kernel, dim3(2 * pairs), THREADS, smem, stream, 1, dy, w, x, out[0], out[1], p) == cudaSuccess
+               ? FP4ATTN_OK
+               : FP4ATTN_ERR_CUDA;
 }
 
 }  // namespace
@@ -480,8 +485,8 @@ int launch_linear_backward(const LinearBwdArgs& a, cudaStream_t stream) {
         for (int i = 0; i < 2; ++i)
             if (p.prod[i].split > 1) n += (long long)p.prod[i].rows * (a.K / 8);
         const long long grid = (n + 255) / 256;
-        join_parts_kernel<<<(unsigned)(grid < 1184 ? grid : 1184), 256, 0, stream>>>(p);
-        if (cudaGetLastError() != cudaSuccess) return FP4ATTN_ERR_CUDA;
+        if (launch_behind(join_parts_kernel, dim3((unsigned)(grid < 1184 ? grid : 1184)), 256, 0, stream, 1, p) != cudaSuccess)
+            return FP4ATTN_ERR_CUDA;
     }
     return FP4ATTN_OK;
 }

@@ -64,18 +64,6 @@ __device__ __forceinline__ uint4 pack(const float2 (&v)[4]) {
 __device__ __forceinline__ uint2 pack(const float2 (&v)[2]) { return make_uint2(pack_pair(v[0]), pack_pair(v[1])); }
 __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
-// Largest magnitudes of a unit of bf16 values, a pair in a word, NaN kept.
-__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
-    uint32_t m;
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
-    return m;
-}
-__device__ __forceinline__ uint32_t abs_pair(uint32_t a) { return a & 0x7FFF7FFFu; }
-__device__ __forceinline__ uint32_t amax_pair(uint2 w) { return max_pair(abs_pair(w.x), abs_pair(w.y)); }
-__device__ __forceinline__ uint32_t amax_pair(uint4 w) {
-    return max_pair(amax_pair(make_uint2(w.x, w.y)), amax_pair(make_uint2(w.z, w.w)));
-}
-
 // Residual units in shared or global memory.
 __device__ __forceinline__ void load_res(const void* row, int u, float2 (&v)[4]) {
     unpack(static_cast<const uint4*>(row)[u], v);
@@ -230,6 +218,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) norm_gate_kernel(const __grid_
     team.rank = WIDE ? cluster_ctarank() : 0;
     team.ranks = WIDE ? cluster_nctarank() : 1;
     const int c0 = first_column(a.cols, team.rank), cols = min(a.cols, a.C - c0), NU = cols / U;
+    pdl_wait();
+    pdl_trigger();
     const float gz = QUANT ? (a.gz ? __ldg(a.gz) : 1.0f) : 1.0f;
     if (QUANT) make_scale_table(table, gz, threadIdx.x);
     if (threadIdx.x == 0) abort_all = 0;
@@ -539,6 +529,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) norm_gate_bwd_kernel(const __grid
     __syncthreads();
     if constexpr (WIDE) cluster_sync();
     volatile int* abort_flag = &abort_all;
+    pdl_wait();
+    pdl_trigger();
 
     const bool has_h = a.h != nullptr, has_dy = a.dy != nullptr;
     const uint32_t res_bytes = (uint32_t)cols * ES, half_bytes = (uint32_t)cols * 2;
@@ -779,6 +771,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) norm_gate_bwd_kernel(const __grid
 // in the first part's place, for norm_weights_kernel.
 __global__ void __launch_bounds__(256) norm_join_kernel(const __grid_constant__ NormBwdArgs a) {
     __shared__ float sum[3][8][32];
+    pdl_wait();
+    pdl_trigger();
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int64_t blocks = (a.C + 31) / 32;
     const int64_t g = blockIdx.x / blocks, c = (blockIdx.x - g * blocks) * 32 + tx;
@@ -817,6 +811,8 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const __grid_constant__ 
 
 __global__ void __launch_bounds__(256) norm_weights_kernel(const __grid_constant__ NormBwdArgs a) {
     __shared__ float sum[2][8][32];
+    pdl_wait();
+    pdl_trigger();
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + tx;
     float s[2] = {0.0f, 0.0f};
@@ -890,20 +886,9 @@ int shape_of(const void* kernel, const Split& s, int teams, size_t fixed_bytes, 
 
 template <typename Args>
 int launch(void (*kernel)(Args), const Args& a, int threads, const Split& s, const Shape& sh, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(sh.grid);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = sh.smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    if (s.ctas > 1) {
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)s.ctas;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-    }
-    return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? FP4ATTN_OK : FP4ATTN_ERR_CUDA;
+    return launch_behind(kernel, dim3(sh.grid), (unsigned)threads, sh.smem, stream, (unsigned)s.ctas, a) == cudaSuccess
+               ? FP4ATTN_OK
+               : FP4ATTN_ERR_CUDA;
 }
 
 using FwdKernel = void (*)(const NormArgs);
@@ -983,12 +968,11 @@ int launch_norm_gate_backward(const NormBwdArgs& a0, bool f32, cudaStream_t stre
     a.slots = sh.slots;
     if (launch(kernel, a, NTHREADS, s, sh, stream) != FP4ATTN_OK) return FP4ATTN_ERR_CUDA;
     const int64_t blocks = (a.C + 31) / 32;
-    norm_join_kernel<<<(unsigned)(blocks * a.groups), 256, 0, stream>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return FP4ATTN_ERR_CUDA;
-    if (a.groups > 1 && (a.dpre || a.dpost)) {
-        norm_weights_kernel<<<(unsigned)blocks, 256, 0, stream>>>(a);
-        if (cudaGetLastError() != cudaSuccess) return FP4ATTN_ERR_CUDA;
-    }
+    if (launch_behind(norm_join_kernel, dim3((unsigned)(blocks * a.groups)), 256, 0, stream, 1, a) != cudaSuccess)
+        return FP4ATTN_ERR_CUDA;
+    if (a.groups > 1 && (a.dpre || a.dpost) &&
+        launch_behind(norm_weights_kernel, dim3((unsigned)blocks), 256, 0, stream, 1, a) != cudaSuccess)
+        return FP4ATTN_ERR_CUDA;
     return FP4ATTN_OK;
 }
 

@@ -9,6 +9,30 @@
 
 namespace fp4attn {
 
+// Launch that may start before the kernel in front of it has finished (see
+// pdl_wait): hides most of a launch's latency in chains of short kernels.
+template <typename... P, typename... A>
+inline cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
+                                 unsigned cluster, const A&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cluster > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = cluster;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // Scales of a matrix of `rows` x K values lie in tiles of 128 rows x 64
 // channels (four blocks), 512 bytes each, tiles of one row block in channel
 // order: the word of row r and 64-channel chunk c (its four scales) is word
@@ -29,6 +53,18 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     float d;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
+}
+
+// Largest magnitudes of a unit of bf16 values, a pair in a word, NaN kept.
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
+    uint32_t m;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+    return m;
+}
+__device__ __forceinline__ uint32_t abs_pair(uint32_t a) { return a & 0x7FFF7FFFu; }
+__device__ __forceinline__ uint32_t amax_pair(uint2 w) { return max_pair(abs_pair(w.x), abs_pair(w.y)); }
+__device__ __forceinline__ uint32_t amax_pair(uint4 w) {
+    return max_pair(amax_pair(make_uint2(w.x, w.y)), amax_pair(make_uint2(w.z, w.w)));
 }
 
 // Scale byte and reciprocal of one block with largest magnitude a:
@@ -94,15 +130,6 @@ __device__ __forceinline__ void row_block_scale(const ScaleTable& tab, float gue
     } else {
         row_block_scale(a, g, s, inv);
     }
-}
-
-// Codes of eight values times inv.
-__device__ __forceinline__ uint32_t row_codes8(const float (&v)[8], float inv) {
-    const float2 i2 = make_float2(inv, inv);
-    float2 r[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) r[k] = __fmul2_rn(make_float2(v[2 * k], v[2 * k + 1]), i2);
-    return cvt_e2m1x8(r[0].x, r[0].y, r[1].x, r[1].y, r[2].x, r[2].y, r[3].x, r[3].y);
 }
 
 // Smallest computed per-tensor scale and the value it covers.

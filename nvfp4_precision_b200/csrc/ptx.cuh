@@ -19,6 +19,14 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
     return t;
 }
 
+// Launches with programmatic stream serialisation (launch_behind): a kernel may
+// start before the one in front of it has finished.  pdl_wait returns when that
+// one is complete and its writes are visible; pdl_trigger lets the next kernel
+// start.  A kernel triggers behind its own wait, so that whatever a kernel does
+// before its wait finds everything up to the second last kernel complete.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- mbarrier --
 
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
