@@ -209,10 +209,6 @@ struct QuantRowsArgs {
 cudaError_t launch_quantize_rows(const QuantRowsArgs& a, bool f32, cudaStream_t stream);
 cudaError_t launch_dequant_rows(const uint8_t* codes, const uint8_t* scales, const float* g, int64_t rows, int64_t K,
                                 void* out, bool f32, cudaStream_t stream);
-// part: COLSUM_PARTS * cols floats
-cudaError_t launch_column_sums(const __nv_bfloat16* x, int64_t ld, int64_t rows, int64_t cols, float* part, float* out,
-                               cudaStream_t stream);
-
 // out[m][n] = g_x g_w sum_k x[m][k] w[n][k] + bias[n] over NVFP4 operands.
 struct GemmFp4Args {
     const uint8_t* x_codes;
@@ -252,6 +248,13 @@ struct LinearBwdArgs {
     float* part;            // linear_backward_part_bytes
     int* status;
 };
+// Blocks of its first launch, by what they do.
+struct BwdPrepare {
+    int sums, strips;        // partial column sums: strips of 256 columns times parts
+    int64_t rows_per_part;
+    int w_tiles;             // 128 x 128 tiles of w; the rest are x's
+};
+cudaError_t launch_backward_prepare(const LinearBwdArgs& a, int& colsum_parts, cudaStream_t stream);
 size_t linear_backward_part_bytes(int64_t M, int64_t N, int64_t K);
 int launch_linear_backward(const LinearBwdArgs& a, cudaStream_t stream);
 

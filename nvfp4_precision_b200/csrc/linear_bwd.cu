@@ -39,9 +39,11 @@ constexpr int PAIRS = 74;  // of 148 SMs
 
 template <int TN>
 struct Cfg {
-    static constexpr uint32_t A_BYTES = 2 * PANEL;               // 128 rows (or columns) of A per CTA
-    static constexpr uint32_t B_BYTES = (TN / 128) * PANEL;      // TN / 2 columns of B per CTA
-    static constexpr uint32_t STAGE = A_BYTES + B_BYTES;
+    static constexpr int N = TN < 256 ? TN : 256;            // columns of one accumulator
+    static constexpr int HALVES = TN / N;                    // accumulators of a tile
+    static constexpr uint32_t A_BYTES = 2 * PANEL;           // 128 rows (or columns) of A per CTA
+    static constexpr uint32_t B_HALF = (N / 128) * PANEL;    // N / 2 columns of B per CTA
+    static constexpr uint32_t STAGE = A_BYTES + HALVES * B_HALF;
     static constexpr int STAGES = (int)(193u * 1024 / STAGE) < 8 ? (int)(193u * 1024 / STAGE) : 8;
 };
 
@@ -58,19 +60,24 @@ struct Product {
     int rows;         // rows of the output
     int contraction;
     int row_tiles;
-    int split;        // parts of the contraction
-    int units;        // row_tiles * col_tiles * split
+    int whole;        // tiles done at once; the ones behind them are split
+    int split;        // into parts of the contraction
+    int units;        // whole + split * (tiles - whole)
     int a_mn;         // A is MN-major (dy^T)
     const float* g;
     __nv_bfloat16* out;
     long long ld;
-    float* part;      // [split][rows][K] when split > 1
+    float* part;      // [tiles - whole][split][BM][TN]
 };
 
 struct BwdGemmParams {
     Product prod[2];
     int K;            // output columns of both
-    int col_tiles;
+    int col_tiles, tn;
+    // dbias: column sums of dy, from their parts
+    const float* colsum_part;
+    int colsum_parts, N;
+    float* dbias;
     int* status;
 };
 
@@ -94,21 +101,39 @@ __device__ __forceinline__ void tile_of(int t, int row_tiles, int col_tiles, int
 }
 
 struct Unit {
-    int which, rt, ct, part, s_begin, s_end;
+    int which, rt, ct, s_begin, s_end;
+    int part;  // index into the product's parts, -1 for a whole tile
 };
 __device__ __forceinline__ Unit unit_of(const BwdGemmParams& p, int u) {
     Unit w;
     w.which = u >= p.prod[0].units;
     const Product& q = p.prod[w.which];
     const int v = w.which ? u - p.prod[0].units : u;
-    const int tiles = q.row_tiles * p.col_tiles;
-    w.part = v / tiles;
-    tile_of(v - w.part * tiles, q.row_tiles, p.col_tiles, w.rt, w.ct);
     const int stages = (q.contraction + BKC - 1) / BKC;
-    w.s_begin = (int)((long long)stages * w.part / q.split);
-    w.s_end = (int)((long long)stages * (w.part + 1) / q.split);
+    if (v < q.whole) {
+        tile_of(v, q.row_tiles, p.col_tiles, w.rt, w.ct);
+        w.part = -1;
+        w.s_begin = 0;
+        w.s_end = stages;
+    } else {
+        // the parts of a tile lie far apart: neighbours read the same contraction
+        const int tail = q.row_tiles * p.col_tiles - q.whole;
+        const int k = (v - q.whole) / tail, i = v - q.whole - k * tail;
+        tile_of(q.whole + i, q.row_tiles, p.col_tiles, w.rt, w.ct);
+        w.part = i * q.split + k;
+        w.s_begin = (int)((long long)stages * k / q.split);
+        w.s_end = (int)((long long)stages * (k + 1) / q.split);
+    }
     return w;
 }
+
+// Which accumulator half h of a CTA's tile number `local` takes, and for the
+// how-manieth time it is taken: tiles of 512 columns take both, narrower ones
+// take turns.
+template <int TN>
+__device__ __forceinline__ int acc_of(int local, int h) { return TN > 256 ? h : local & 1; }
+template <int TN>
+__device__ __forceinline__ int use_of(int local) { return TN > 256 ? local : local >> 1; }
 
 template <int TN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
@@ -164,7 +189,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             const Unit w = unit_of(p, u);
             const bool a_mn = p.prod[w.which].a_mn != 0;
             const int row0 = BM * w.rt + 128 * (int)rank;
-            const int col0 = TN * w.ct + TN / 2 * (int)rank;
+            const int col0 = TN * w.ct + C::N / 2 * (int)rank;
             const CUtensorMap* tb = a_mn ? &tm_x : &tm_w;
             for (int ks = w.s_begin; ks < w.s_end; ++ks, ++it) {
                 const int slot = it % C::STAGES;
@@ -184,8 +209,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                         tma_load_2d_2cta(at + PANEL * i, &tm_dy, a_mn ? row0 + 64 * i : k0, a_mn ? k0 : row0 + 64 * i,
                                          full);
 #pragma unroll
-                    for (int j = 0; j < TN / 128; ++j)
-                        tma_load_2d_2cta(at + C::A_BYTES + PANEL * j, tb, col0 + 64 * j, k0, full);
+                    for (int h = 0; h < C::HALVES; ++h)
+#pragma unroll
+                        for (int j = 0; j < C::N / 128; ++j)
+                            tma_load_2d_2cta(at + C::A_BYTES + C::B_HALF * h + PANEL * j, tb, col0 + C::N * h + 64 * j, k0,
+                                             full);
                 }
                 __syncwarp();
             }
@@ -198,7 +226,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (rank == 0) {
             const bool leader = elect_one_sync();
             // kind::f16, fp32 accumulator, bf16 operands, B MN-major (1 << 16), M = 256
-            constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(TN >> 3) << 17) |
+            constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(C::N >> 3) << 17) |
                                        ((uint32_t)(BM >> 4) << 24);
             auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
                 return __all_sync(0xffffffffu, mbar_wait_spin(bar, parity, abort_flag, p.status, kLimitNs));
@@ -213,28 +241,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 // panels PANEL apart, 8-row groups 1 KB apart, 16 rows 2 KB on
                 const uint32_t a_lbo = a_mn ? PANEL : 16u;
                 const uint64_t a_step = a_mn ? 2048u >> 4 : 32u >> 4;
-                const uint32_t acc = tmem + (local & 1 ? 256u : 0u);
-                if (local >= 2 && !wait(smem_u32(&sm.acc_empty[local & 1]), ((local >> 1) - 1) & 1)) break;
-                tc_fence_after();
-                for (int ks = w.s_begin; ks < w.s_end; ++ks, ++it) {
+                for (int ks = w.s_begin; ok && ks < w.s_end; ++ks, ++it) {
                     const int slot = it % C::STAGES;
                     if (!wait(smem_u32(&sm.full[slot]), (it / C::STAGES) & 1)) {
                         ok = false;
                         break;
                     }
-                    if (leader) {
-                        tc_fence_after();
-                        const uint32_t at = ring_u + C::STAGE * slot;
-                        const uint64_t ad = smem_desc(at, a_lbo, 1024, LAYOUT_SW128);
-                        const uint64_t bd = smem_desc(at + C::A_BYTES, PANEL, 1024, LAYOUT_SW128);
 #pragma unroll
-                        for (int k = 0; k < BKC / 16; ++k)
-                            mma_bf16_ss_2cta(acc, ad + a_step * k, bd + (2048u >> 4) * k, idesc,
-                                             (ks > w.s_begin || k > 0) ? 1u : 0u);
-                        tc_commit_2cta(smem_u32(&sm.empty[slot]));
-                        if (ks == w.s_end - 1) tc_commit_2cta(smem_u32(&sm.acc_full[local & 1]));
+                    for (int h = 0; h < C::HALVES; ++h) {
+                        const int buf = acc_of<TN>(local, h), use = use_of<TN>(local);
+                        if (ks == w.s_begin && use > 0 && !wait(smem_u32(&sm.acc_empty[buf]), (use - 1) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        if (leader) {
+                            tc_fence_after();
+                            const uint32_t at = ring_u + C::STAGE * slot;
+                            const uint64_t ad = smem_desc(at, a_lbo, 1024, LAYOUT_SW128);
+                            const uint64_t bd = smem_desc(at + C::A_BYTES + C::B_HALF * h, PANEL, 1024, LAYOUT_SW128);
+#pragma unroll
+                            for (int k = 0; k < BKC / 16; ++k)
+                                mma_bf16_ss_2cta(tmem + 256u * buf, ad + a_step * k, bd + (2048u >> 4) * k, idesc,
+                                                 (ks > w.s_begin || k > 0) ? 1u : 0u);
+                            if (ks == w.s_end - 1) tc_commit_2cta(smem_u32(&sm.acc_full[buf]));
+                            if (h == C::HALVES - 1) tc_commit_2cta(smem_u32(&sm.empty[slot]));
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
             }
             if (leader) {
@@ -250,51 +283,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
         const uint32_t box = ring_u + C::STAGES * C::STAGE + STORE_BOX * warp;
         int local = 0;
-        for (int u = pair; u < units; u += pairs, ++local) {
+        bool ok = true;
+        for (int u = pair; ok && u < units; u += pairs, ++local) {
             const Unit w = unit_of(p, u);
             const Product& q = p.prod[w.which];
-            const uint32_t acc = tmem + lanes + (local & 1 ? 256u : 0u);
-            if (!warp_wait(smem_u32(&sm.acc_full[local & 1]), (local >> 1) & 1, abort_flag, p.status)) break;
-            tc_fence_after();
             const float g = q.g ? __ldg(q.g) : 1.0f;
             if (u == 0 && threadIdx.x == 0 && rank == 0) {
                 const float g1 = p.prod[1].g ? __ldg(p.prod[1].g) : 1.0f;
                 if (bad_gscale(g) || bad_gscale(g1)) raise_status(p.status, FP4ATTN_ERR_RANGE);
             }
-            const int row0 = BM * w.rt + 128 * (int)rank + 32 * quarter, row = row0 + lane;
+            const int in_tile = 128 * (int)rank + 32 * quarter, row0 = BM * w.rt + in_tile;
 #pragma unroll 1
-            for (int i = 0; i < TN / 128; ++i) {
-                const int c0 = TN / 2 * half + 64 * i, col = TN * w.ct + c0;
-                uint32_t r[2][32];
-                tmem_ld32(acc + c0, r[0]);
-                tmem_ld32(acc + c0 + 32, r[1]);
-                tmem_wait_ld();
-                if (i == TN / 128 - 1) {
-                    tc_fence_before();
+            for (int h = 0; h < C::HALVES; ++h) {
+                const int buf = acc_of<TN>(local, h);
+                if (!warp_wait(smem_u32(&sm.acc_full[buf]), use_of<TN>(local) & 1, abort_flag, p.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t acc = tmem + lanes + 256u * buf;
+#pragma unroll 1
+                for (int i = 0; i < C::N / 128; ++i) {
+                    const int c0 = C::N / 2 * half + 64 * i, in_col = C::N * h + c0, col = TN * w.ct + in_col;
+                    uint32_t r[2][32];
+                    tmem_ld32(acc + c0, r[0]);
+                    tmem_ld32(acc + c0 + 32, r[1]);
+                    tmem_wait_ld();
+                    if (i == C::N / 128 - 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&sm.acc_empty[buf]), 0));
+                    }
+                    if (w.part >= 0) {
+                        // fp32, the tile's whole rows: what lies past the matrix is never read
+                        float4* dst = reinterpret_cast<float4*>(
+                            q.part + ((long long)w.part * BM + in_tile + lane) * TN + in_col);
+                        if (FP4ATTN_IN_BOUNDS(w.part < q.split * (q.row_tiles * p.col_tiles - q.whole), p.status))
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                dst[k] = make_float4(__uint_as_float(r[k / 8][4 * (k % 8)]),
+                                                     __uint_as_float(r[k / 8][4 * (k % 8) + 1]),
+                                                     __uint_as_float(r[k / 8][4 * (k % 8) + 2]),
+                                                     __uint_as_float(r[k / 8][4 * (k % 8) + 3]));
+                    } else {
+                        uint32_t v[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            v[k] = pack_bf16x2(__uint_as_float(r[k / 16][2 * (k % 16)]) * g,
+                                               __uint_as_float(r[k / 16][2 * (k % 16) + 1]) * g);
+                        store_box(w.which ? &tm_out1 : &tm_out0, box, v, row0, col, q.rows, p.K, lane);
+                    }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&sm.acc_empty[local & 1]), 0));
                 }
-                if (q.split > 1) {
-                    // K is a multiple of 32
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (row < q.rows && col + 32 * h < p.K && FP4ATTN_IN_BOUNDS(w.part < q.split, p.status)) {
-                            float4* dst =
-                                reinterpret_cast<float4*>(q.part + ((long long)w.part * q.rows + row) * p.K + col + 32 * h);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                dst[k] = make_float4(__uint_as_float(r[h][4 * k]), __uint_as_float(r[h][4 * k + 1]),
-                                                     __uint_as_float(r[h][4 * k + 2]), __uint_as_float(r[h][4 * k + 3]));
-                        }
-                } else {
-                    uint32_t v[32];
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        v[k] = pack_bf16x2(__uint_as_float(r[k / 16][2 * (k % 16)]) * g,
-                                           __uint_as_float(r[k / 16][2 * (k % 16) + 1]) * g);
-                    store_box(w.which ? &tm_out1 : &tm_out0, box, v, row0, col, q.rows, p.K, lane);
-                }
-                __syncwarp();
             }
         }
         store_box_finish(lane);
@@ -308,27 +348,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
 }
 
-// out = g * (sum of the parts, in order), eight columns per thread.
-__global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ BwdGemmParams p) {
+// The last launch: dbias = sum of the partial column sums, and the split tiles'
+// out = g * (sum of the parts), all in order.  A CTA takes 2048 / tn rows of a
+// tile at a time, a thread eight columns.
+__global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ BwdGemmParams p, const int sum_blocks) {
     pdl_wait();
     pdl_trigger();
-    const long long per_row = p.K / 8;
-    const long long n0 = p.prod[0].split > 1 ? p.prod[0].rows * per_row : 0;
-    const long long n1 = p.prod[1].split > 1 ? p.prod[1].rows * per_row : 0;
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n0 + n1; i += (long long)gridDim.x * 256) {
-        const Product& q = p.prod[i >= n0];
-        const long long j = i >= n0 ? i - n0 : i;
-        const long long row = j / per_row, col = 8 * (j - row * per_row);
+    if ((int)blockIdx.x < sum_blocks) {
+        // 64 columns by four shares of the parts, which meet in order
+        __shared__ float sum[4][64];
+        const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6, c = blockIdx.x * 64 + tx;
+        float s = 0.0f;
+        if (c < p.N) {
+            const int k0 = p.colsum_parts * ty / 4, k1 = p.colsum_parts * (ty + 1) / 4;
+#pragma unroll 8
+            for (int k = k0; k < k1; ++k) s += __ldcg(p.colsum_part + (long long)k * p.N + c);
+        }
+        sum[ty][tx] = s;
+        __syncthreads();
+        if (ty == 0 && c < p.N) p.dbias[c] = (sum[0][tx] + sum[1][tx]) + (sum[2][tx] + sum[3][tx]);
+        return;
+    }
+    const int per_row = p.tn / 8, rows = 256 / per_row, groups = BM / rows;
+    const int tail0 = p.prod[0].row_tiles * p.col_tiles - p.prod[0].whole;
+    const int tail1 = p.prod[1].row_tiles * p.col_tiles - p.prod[1].whole;
+    for (int b = (int)blockIdx.x - sum_blocks; b < (tail0 + tail1) * groups; b += (int)gridDim.x - sum_blocks) {
+        const int t = b / groups;
+        const Product& q = p.prod[t >= tail0];
+        const int i = t >= tail0 ? t - tail0 : t;
+        int rt, ct;
+        tile_of(q.whole + i, q.row_tiles, p.col_tiles, rt, ct);
+        const int in_row = (b - t * groups) * rows + (int)threadIdx.x / per_row, in_col = (int)threadIdx.x % per_row * 8;
+        const int row = BM * rt + in_row, col = p.tn * ct + in_col;
+        if (row >= q.rows || col >= p.K) continue;
         float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll 4
         for (int k = 0; k < q.split; ++k) {
-            const float4* src = reinterpret_cast<const float4*>(q.part + ((long long)k * q.rows + row) * p.K + col);
+            const float4* src =
+                reinterpret_cast<const float4*>(q.part + ((long long)(i * q.split + k) * BM + in_row) * p.tn + in_col);
             const float4 lo = __ldcg(src), hi = __ldcg(src + 1);
             s[0] += lo.x, s[1] += lo.y, s[2] += lo.z, s[3] += lo.w;
             s[4] += hi.x, s[5] += hi.y, s[6] += hi.z, s[7] += hi.w;
         }
         const float g = q.g ? __ldg(q.g) : 1.0f;
-        if (FP4ATTN_IN_BOUNDS(row < q.rows, p.status))
+        if (FP4ATTN_IN_BOUNDS(row < q.rows && col + 8 <= p.K, p.status))
             *reinterpret_cast<uint4*>(q.out + row * q.ld + col) =
                 make_uint4(pack_bf16x2(g * s[0], g * s[1]), pack_bf16x2(g * s[2], g * s[3]),
                            pack_bf16x2(g * s[4], g * s[5]), pack_bf16x2(g * s[6], g * s[7]));
@@ -344,58 +407,86 @@ bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int6
                              CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// How the two products (dw, then dx) are cut up.
 struct Plan {
     int tn;
-    int split[2];  // dw, dx
+    int64_t tiles[2], whole[2];
+    int split[2];
+    int first;  // the product whose units go first: the longer ones
 };
 
 // Tile width and splits by a model of the launch in clocks: units go round the
-// pairs, the products with the longer contraction first.
+// pairs in order, so a pair has the longest way to go that starts first.  Either
+// all tiles of a small product are split, or the last ones, which do not fill a
+// round of the pairs any more.  A stage costs what its bytes take (48, 32 or 24
+// KB at about 42 bytes a clock), a unit its epilogue's part that nothing hides.
 Plan make_plan(int64_t M, int64_t N, int64_t K, bool want_dw, bool want_dx) {
-    Plan best{256, {1, 1}};
+    Plan best{};
     double best_cost = -1.0;
     const int64_t rows[2] = {want_dw ? N : 0, want_dx ? M : 0}, contraction[2] = {M, N};
-    static const int splits[8] = {1, 2, 3, 4, 6, 8, 12, 16};
-    for (int tn = 256; tn >= 128; tn -= 128) {
-        const double per_stage = tn == 256 ? 512.0 : 288.0, per_unit = 1500.0;
+    for (int tn = 512; tn >= 128; tn /= 2) {
+        const double per_stage = tn == 512 ? 1170.0 : tn == 256 ? 780.0 : 585.0, per_unit = tn == 512 ? 4000.0 : 1500.0;
         const int64_t ct = (K + tn - 1) / tn;
         int64_t tiles[2], stages[2];
         for (int i = 0; i < 2; ++i) {
             tiles[i] = (rows[i] + BM - 1) / BM * ct;
             stages[i] = (contraction[i] + BKC - 1) / BKC;
         }
-        const bool may_split = tiles[0] + tiles[1] < 2 * PAIRS;
-        for (int a = 0; a < (may_split ? 8 : 1); ++a) {
-            for (int b = 0; b < (may_split ? 8 : 1); ++b) {
-                const int s[2] = {splits[a], splits[b]};
-                if ((a && (s[0] * 2 > stages[0] || !tiles[0])) || (b && (s[1] * 2 > stages[1] || !tiles[1]))) continue;
-                double unit[2], join = 0.0;
-                int64_t n[2];
-                for (int i = 0; i < 2; ++i) {
-                    unit[i] = (double)((stages[i] + s[i] - 1) / s[i]) * per_stage + per_unit;
-                    n[i] = tiles[i] * s[i];
-                    if (s[i] > 1) join += 4000.0 + (double)s[i] * rows[i] * K * 8.0 / 4000.0;
-                }
-                const int first = unit[0] >= unit[1] ? 0 : 1;
-                const int64_t n0 = (n[first] + PAIRS - 1) / PAIRS, all = (n[0] + n[1] + PAIRS - 1) / PAIRS;
-                const double cost = (double)n0 * unit[first] + (double)(all - n0) * unit[1 - first] + join;
-                if (best_cost < 0.0 || cost < best_cost) {
-                    best_cost = cost;
-                    best.tn = tn;
-                    best.split[0] = s[0];
-                    best.split[1] = s[1];
-                }
+        auto unit = [&](int i, int split) { return (double)((stages[i] + split - 1) / split) * per_stage + per_unit; };
+        auto join = [&](int64_t tail, int split) { return 4000.0 + (double)tail * split * BM * tn * 8.0 / 4000.0; };
+        auto offer = [&](double cost, const int64_t (&whole)[2], const int (&split)[2], int first) {
+            if (best_cost >= 0.0 && cost >= best_cost) return;
+            best_cost = cost;
+            best = Plan{tn, {tiles[0], tiles[1]}, {whole[0], whole[1]}, {split[0], split[1]}, first};
+        };
+        // the last tiles of the product that goes second
+        const int first = (tiles[0] && (!tiles[1] || stages[0] >= stages[1])) ? 0 : 1, second = 1 - first;
+        const int last = tiles[second] ? second : first;
+        const int64_t total = tiles[0] + tiles[1], rest = total % PAIRS;
+        {
+            const double head = (double)((tiles[first] + PAIRS - 1) / PAIRS);
+            const double rounds = (double)((total + PAIRS - 1) / PAIRS);
+            offer(head * unit(first, 1) + (rounds - head) * unit(second, 1), tiles, {1, 1}, first);
+        }
+        int s = rest ? (int)(PAIRS / rest) : 1;
+        if (s > 16) s = 16;
+        if (s > stages[last] / 2) s = (int)(stages[last] / 2);
+        if (s >= 2 && total > rest && rest <= tiles[last]) {
+            int64_t whole[2] = {tiles[0], tiles[1]};
+            whole[last] -= rest;
+            int split[2] = {1, 1};
+            split[last] = s;
+            const int64_t n = whole[0] + whole[1];
+            const double head = (double)((whole[first] + PAIRS - 1) / PAIRS);
+            offer(head * unit(first, 1) + ((double)(n / PAIRS) - head) * unit(second, 1) + unit(last, s) + join(rest, s),
+                  whole, split, first);
+        }
+        if (total >= 2 * PAIRS) continue;
+        double unit_cost[2][5], join_cost[2][5];
+        for (int i = 0; i < 2; ++i)
+            for (int k = 0; k < 5; ++k) {
+                const bool may = k == 0 || (tiles[i] && (2 << k) <= stages[i]);
+                unit_cost[i][k] = may ? unit(i, 1 << k) : -1.0;
+                join_cost[i][k] = k ? join(tiles[i], 1 << k) : 0.0;
+            }
+        for (int a = 0; a < 5 && unit_cost[0][a] >= 0.0; ++a) {
+            for (int b = 0; b < 5 && unit_cost[1][b] >= 0.0; ++b) {
+                const int64_t n[2] = {tiles[0] << a, tiles[1] << b}, all = n[0] + n[1];
+                if (all > 4 * PAIRS) break;
+                const double u0 = unit_cost[0][a], u1 = unit_cost[1][b];
+                const int f = (n[0] && (!n[1] || u0 >= u1)) ? 0 : 1;
+                const int64_t head = (n[f] + PAIRS - 1) / PAIRS, rounds = (all + PAIRS - 1) / PAIRS;
+                offer(join_cost[0][a] + join_cost[1][b] + (double)head * (f ? u1 : u0) +
+                          (double)(rounds - head) * (f ? u0 : u1),
+                      {a ? 0 : tiles[0], b ? 0 : tiles[1]}, {1 << a, 1 << b}, f);
             }
         }
     }
     return best;
 }
 
-int64_t part_floats(const Plan& pl, int64_t M, int64_t N, int64_t K, bool want_dw, bool want_dx) {
-    int64_t n = 0;
-    if (want_dw && pl.split[0] > 1) n += pl.split[0] * N * K;
-    if (want_dx && pl.split[1] > 1) n += pl.split[1] * M * K;
-    return n;
+int64_t part_floats(const Plan& pl) {
+    return ((pl.tiles[0] - pl.whole[0]) * pl.split[0] + (pl.tiles[1] - pl.whole[1]) * pl.split[1]) * BM * pl.tn;
 }
 
 template <int TN>
@@ -418,7 +509,7 @@ size_t linear_backward_part_bytes(int64_t M, int64_t N, int64_t K) {
     int64_t most = 0;
     for (int want = 1; want < 4; ++want) {
         const bool dw = want & 1, dx = want & 2;
-        const int64_t n = part_floats(make_plan(M, N, K, dw, dx), M, N, K, dw, dx);
+        const int64_t n = part_floats(make_plan(M, N, K, dw, dx));
         most = n > most ? n : most;
     }
     return (size_t)most * 4;
@@ -429,23 +520,23 @@ int launch_linear_backward(const LinearBwdArgs& a, cudaStream_t stream) {
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return FP4ATTN_ERR_CUDA;
-    // the operands' unit-scale values
-    if (a.dx && launch_dequant_rows(a.w_codes, a.w_scales, nullptr, a.N, a.K, a.w_bf16, false, stream) != cudaSuccess)
-        return FP4ATTN_ERR_CUDA;
-    if (a.dw && launch_dequant_rows(a.x_codes, a.x_scales, nullptr, a.M, a.K, a.x_bf16, false, stream) != cudaSuccess)
-        return FP4ATTN_ERR_CUDA;
-    if (a.dbias && launch_column_sums(a.dy, a.ld_dy, a.M, a.N, a.colsum_part, a.dbias, stream) != cudaSuccess)
-        return FP4ATTN_ERR_CUDA;
-    if (!a.dx && !a.dw) return FP4ATTN_OK;
+    if (!a.dx && !a.dw && !a.dbias) return FP4ATTN_OK;
+    int colsum_parts = 0;
+    if (launch_backward_prepare(a, colsum_parts, stream) != cudaSuccess) return FP4ATTN_ERR_CUDA;
     const Plan pl = make_plan(a.M, a.N, a.K, a.dw != nullptr, a.dx != nullptr);
     BwdGemmParams p{};
     p.K = (int)a.K;
+    p.tn = pl.tn;
     p.col_tiles = (int)((a.K + pl.tn - 1) / pl.tn);
+    p.colsum_part = a.colsum_part;
+    p.colsum_parts = colsum_parts;
+    p.N = (int)a.N;
+    p.dbias = a.dbias;
     p.status = a.status;
     float* part = a.part;
-    Product prod[2]{};
+    int tail = 0;
     for (int i = 0; i < 2; ++i) {
-        Product& q = prod[i];
+        Product& q = p.prod[i == pl.first ? 0 : 1];
         const bool dw = i == 0;
         q.rows = (int)(dw ? a.N : a.M);
         q.contraction = (int)(dw ? a.M : a.N);
@@ -453,41 +544,38 @@ int launch_linear_backward(const LinearBwdArgs& a, cudaStream_t stream) {
         q.g = dw ? a.gx : a.gw;
         q.out = dw ? a.dw : a.dx;
         q.ld = dw ? a.K : a.ld_dx;
-        q.split = pl.split[i];
         q.row_tiles = q.out ? (q.rows + BM - 1) / BM : 0;
-        q.units = q.row_tiles * p.col_tiles * q.split;
-        if (!q.out) q.split = 1;
-        if (q.split > 1) {
-            q.part = part;
-            part += (long long)q.split * q.rows * a.K;
-        }
+        q.whole = (int)pl.whole[i];
+        q.split = pl.split[i];
+        const int split_tiles = (int)(pl.tiles[i] - pl.whole[i]);
+        q.units = q.whole + split_tiles * q.split;
+        q.part = part;
+        part += (long long)split_tiles * q.split * BM * pl.tn;
+        tail += split_tiles;
     }
-    const auto stages = [](const Product& q) { return (q.contraction + BKC - 1) / BKC / q.split; };
-    const int first = (prod[0].units && (!prod[1].units || stages(prod[0]) >= stages(prod[1]))) ? 0 : 1;
-    p.prod[0] = prod[first];
-    p.prod[1] = prod[1 - first];
-    CUtensorMap dy, w, x;
-    if (!make_map(&dy, a.dy, a.M, a.N, a.ld_dy)) return FP4ATTN_ERR_CUDA;
-    w = x = dy;
-    if (a.dx && !make_map(&w, a.w_bf16, a.N, a.K, a.K)) return FP4ATTN_ERR_CUDA;
-    if (a.dw && !make_map(&x, a.x_bf16, a.M, a.K, a.K)) return FP4ATTN_ERR_CUDA;
-    CUtensorMap out[2] = {dy, dy};  // a split product, or an absent one, does not use its own
-    for (int i = 0; i < 2; ++i)
-        if (p.prod[i].units && !make_store_map(&out[i], p.prod[i].out, p.prod[i].rows, a.K, p.prod[i].ld))
-            return FP4ATTN_ERR_CUDA;
-    const int units = p.prod[0].units + p.prod[1].units;
-    const int pairs = units < sms / 2 ? units : sms / 2;
-    const int st = pl.tn == 256 ? launch_products<256>(p, dy, w, x, out, pairs, stream)
-                                : launch_products<128>(p, dy, w, x, out, pairs, stream);
-    if (st != FP4ATTN_OK) return st;
-    if (p.prod[0].split > 1 || p.prod[1].split > 1) {
-        long long n = 0;
+    if (a.dx || a.dw) {
+        CUtensorMap dy, w, x;
+        if (!make_map(&dy, a.dy, a.M, a.N, a.ld_dy)) return FP4ATTN_ERR_CUDA;
+        w = x = dy;
+        if (a.dx && !make_map(&w, a.w_bf16, a.N, a.K, a.K)) return FP4ATTN_ERR_CUDA;
+        if (a.dw && !make_map(&x, a.x_bf16, a.M, a.K, a.K)) return FP4ATTN_ERR_CUDA;
+        CUtensorMap out[2] = {dy, dy};  // an absent product does not use its own
         for (int i = 0; i < 2; ++i)
-            if (p.prod[i].split > 1) n += (long long)p.prod[i].rows * (a.K / 8);
-        const long long grid = (n + 255) / 256;
-        if (launch_behind(join_parts_kernel, dim3((unsigned)(grid < 1184 ? grid : 1184)), 256, 0, stream, 1, p) != cudaSuccess)
-            return FP4ATTN_ERR_CUDA;
+            if (p.prod[i].units && !make_store_map(&out[i], p.prod[i].out, p.prod[i].rows, a.K, p.prod[i].ld))
+                return FP4ATTN_ERR_CUDA;
+        const int units = p.prod[0].units + p.prod[1].units;
+        const int pairs = units < sms / 2 ? units : sms / 2;
+        const int st = pl.tn == 512   ? launch_products<512>(p, dy, w, x, out, pairs, stream)
+                       : pl.tn == 256 ? launch_products<256>(p, dy, w, x, out, pairs, stream)
+                                      : launch_products<128>(p, dy, w, x, out, pairs, stream);
+        if (st != FP4ATTN_OK) return st;
     }
+    const int sum_blocks = a.dbias ? (int)((a.N + 63) / 64) : 0;
+    int blocks = tail * pl.tn / 8;  // 2048 / tn rows at a time
+    blocks = blocks < 1184 ? blocks : 1184;
+    if (sum_blocks + blocks > 0 && launch_behind(join_parts_kernel, dim3((unsigned)(sum_blocks + blocks)), 256, 0, stream, 1, p,
+                                                 sum_blocks) != cudaSuccess)
+        return FP4ATTN_ERR_CUDA;
     return FP4ATTN_OK;
 }
 

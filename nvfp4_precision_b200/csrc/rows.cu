@@ -303,14 +303,11 @@ __global__ void __launch_bounds__(Q_THREADS, 1) quantize_rows_kernel(const __gri
 // channels, a thread eight values (16 bytes of bf16, so that a warp's store
 // fills whole sectors) of every sixteenth row.
 template <bool F32>
-__global__ void __launch_bounds__(QTHREADS) dequant_rows_kernel(const uint8_t* __restrict__ codes,
-                                                                const uint8_t* __restrict__ scales, const float* gp,
-                                                                int64_t rows, int64_t K, void* out) {
-    pdl_wait();
-    pdl_trigger();
+__device__ __forceinline__ void dequant_tile(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                                             const float* gp, int64_t rows, int64_t K, void* out, int64_t rb, int64_t cb) {
     const int t = threadIdx.x;
-    const int64_t rb = blockIdx.y, chunks = scale_chunks(K);
-    const int64_t col = (int64_t)blockIdx.x * 128 + 8 * (t & 15);
+    const int64_t chunks = scale_chunks(K);
+    const int64_t col = cb * 128 + 8 * (t & 15);
     if (col >= K) return;
     const uint32_t* words = reinterpret_cast<const uint32_t*>(scales) + (rb * chunks + col / 64) * 128;
     const int row_in = t >> 4, shift = 8 * ((t >> 1) & 3);
@@ -350,23 +347,24 @@ __global__ void __launch_bounds__(QTHREADS) dequant_rows_kernel(const uint8_t* _
     }
 }
 
-// Column sums of bf16 rows [rows][cols] in fp32: CTA (x, y) sums 256 columns
-// (8 per lane) of its share of the rows, its eight warps every eighth row;
-// their sums meet in shared memory in warp order and the CTA writes one row of
-// partial sums, which the second kernel adds in order.  No atomics, so the
-// result does not depend on timing.
-__global__ void __launch_bounds__(256) colsum_part_kernel(const __nv_bfloat16* __restrict__ x, int64_t ld, int64_t rows,
-                                                          int64_t cols, int64_t rows_per_cta, float* part) {
-    __shared__ float sum[8][256];
+template <bool F32>
+__global__ void __launch_bounds__(QTHREADS) dequant_rows_kernel(const uint8_t* codes, const uint8_t* scales, const float* gp,
+                                                                int64_t rows, int64_t K, void* out) {
     pdl_wait();
     pdl_trigger();
+    dequant_tile<F32>(codes, scales, gp, rows, K, out, blockIdx.y, blockIdx.x);
+}
+
+// Column sums of bf16 rows [rows][cols] in fp32, strip `strip` of 256 columns (8
+// per lane) and rows [r0, r1): the warps take every eighth row, their sums meet
+// in shared memory in warp order and leave as one row of partial sums, which are
+// added in order later.  No atomics, so the result does not depend on timing.
+__device__ __forceinline__ void colsum_part(const __nv_bfloat16* __restrict__ x, int64_t ld, int64_t cols, int64_t strip,
+                                            int64_t r0, int64_t r1, float* part, float (&sum)[8][256]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t col = (int64_t)blockIdx.x * 256 + 8 * lane;
-    const int64_t r0 = (int64_t)blockIdx.y * rows_per_cta;
-    const int64_t r1 = (r0 + rows_per_cta < rows) ? r0 + rows_per_cta : rows;
+    const int64_t col = strip * 256 + 8 * lane;
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    const bool whole = col + 8 <= cols;
-    if (whole) {
+    if (col + 8 <= cols) {
 #pragma unroll 4
         for (int64_t r = r0 + warp; r < r1; r += 8) {
             const uint4 w = __ldg(reinterpret_cast<const uint4*>(x + r * ld + col));
@@ -385,23 +383,36 @@ __global__ void __launch_bounds__(256) colsum_part_kernel(const __nv_bfloat16* _
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum[warp][8 * lane + i] = acc[i];
     __syncthreads();
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t c = strip * 256 + threadIdx.x;
     if (c < cols) {
         float s = 0.0f;
 #pragma unroll
         for (int w = 0; w < 8; ++w) s += sum[w][threadIdx.x];
-        part[(int64_t)blockIdx.y * cols + c] = s;
+        part[c] = s;
     }
 }
 
-__global__ void __launch_bounds__(256) colsum_join_kernel(const float* __restrict__ part, int n, int64_t cols, float* out) {
+// What the linear layer's backward needs before its products, in one launch:
+// the unit-scale values of w and x, and the partial column sums of dy.
+__global__ void __launch_bounds__(QTHREADS) backward_prepare_kernel(const __grid_constant__ LinearBwdArgs a,
+                                                                    const __grid_constant__ BwdPrepare n) {
+    __shared__ float sum[8][256];
     pdl_wait();
     pdl_trigger();
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c >= cols) return;
-    float s = 0.0f;
-    for (int i = 0; i < n; ++i) s += part[(int64_t)i * cols + c];
-    out[c] = s;
+    int b = blockIdx.x;
+    if (b < n.sums) {  // first: they read the most
+        const int part = b / n.strips, strip = b - part * n.strips;
+        const int64_t r0 = n.rows_per_part * part, r1 = r0 + n.rows_per_part;
+        colsum_part(a.dy, a.ld_dy, a.N, strip, r0, r1 < a.M ? r1 : a.M, a.colsum_part + (int64_t)part * a.N, sum);
+        return;
+    }
+    b -= n.sums;
+    const int wide = (int)((a.K + 127) / 128);
+    const bool is_w = b < n.w_tiles;
+    if (!is_w) b -= n.w_tiles;
+    const int rb = b / wide, cb = b - rb * wide;
+    dequant_tile<false>(is_w ? a.w_codes : a.x_codes, is_w ? a.w_scales : a.x_scales, nullptr, is_w ? a.N : a.M, a.K,
+                        is_w ? a.w_bf16 : a.x_bf16, rb, cb);
 }
 
 }  // namespace
@@ -456,21 +467,23 @@ cudaError_t launch_dequant_rows(const uint8_t* codes, const uint8_t* scales, con
                          scales, g, rows, K, out);
 }
 
-cudaError_t launch_column_sums(const __nv_bfloat16* x, int64_t ld, int64_t rows, int64_t cols, float* part, float* out,
-                               cudaStream_t stream) {
-    if (cols == 0) return cudaSuccess;
-    if (rows == 0) return cudaMemsetAsync(out, 0, (size_t)cols * 4, stream);
-    const int64_t strips = (cols + 255) / 256;
-    int64_t n = (148 * 4 + strips - 1) / strips;  // about four CTAs per SM
-    const int64_t most = (rows + 63) / 64;
-    n = n < most ? n : most;
-    n = n < COLSUM_PARTS ? n : COLSUM_PARTS;
-    const int64_t per = (rows + n - 1) / n;
-    n = (rows + per - 1) / per;
-    const cudaError_t e = launch_behind(colsum_part_kernel, dim3((unsigned)strips, (unsigned)n), 256, 0, stream, 1, x, ld, rows,
-                                        cols, per, part);
-    if (e != cudaSuccess) return e;
-    return launch_behind(colsum_join_kernel, dim3((unsigned)strips), 256, 0, stream, 1, part, (int)n, cols, out);
+cudaError_t launch_backward_prepare(const LinearBwdArgs& a, int& colsum_parts, cudaStream_t stream) {
+    BwdPrepare n{};
+    const int64_t wide = (a.K + 127) / 128;
+    n.w_tiles = a.dx ? (int)((a.N + 127) / 128 * wide) : 0;
+    const int64_t x_tiles = a.dw ? (a.M + 127) / 128 * wide : 0;
+    colsum_parts = 0;
+    if (a.dbias) {
+        n.strips = (int)((a.N + 255) / 256);
+        int64_t parts = (148 * 4 + n.strips - 1) / n.strips;  // about four CTAs per SM
+        const int64_t most = (a.M + 63) / 64;
+        parts = parts < most ? parts : most;
+        parts = parts < COLSUM_PARTS ? parts : COLSUM_PARTS;
+        n.rows_per_part = (a.M + parts - 1) / parts;
+        colsum_parts = (int)((a.M + n.rows_per_part - 1) / n.rows_per_part);
+        n.sums = n.strips * colsum_parts;
+    }
+    return launch_behind(backward_prepare_kernel, dim3((unsigned)(n.sums + n.w_tiles + x_tiles)), QTHREADS, 0, stream, 1, a, n);
 }
 
 }  // namespace fp4attn
