@@ -246,6 +246,7 @@ int fp4attn_linear_backward(const void* dy, int64_t dy_stride, const uint8_t* x_
     if (!dy || bad_rows(dy, dy_stride, M, N, 8)) return FP4ATTN_ERR_INVALID_ARG;
     if (dx && (!good(w_codes) || !good(w_scales))) return FP4ATTN_ERR_INVALID_ARG;
     if (dw && (!good(x_codes) || !good(x_scales))) return FP4ATTN_ERR_INVALID_ARG;
+    if (!dx && !dw && !dbias) return FP4ATTN_OK;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     LinearBwdArgs a{};
     a.dy = static_cast<const __nv_bfloat16*>(dy);

@@ -520,7 +520,6 @@ int launch_linear_backward(const LinearBwdArgs& a, cudaStream_t stream) {
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return FP4ATTN_ERR_CUDA;
-    if (!a.dx && !a.dw && !a.dbias) return FP4ATTN_OK;
     int colsum_parts = 0;
     if (launch_backward_prepare(a, colsum_parts, stream) != cudaSuccess) return FP4ATTN_ERR_CUDA;
     const Plan pl = make_plan(a.M, a.N, a.K, a.dw != nullptr, a.dx != nullptr);

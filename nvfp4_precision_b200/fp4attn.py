@@ -773,6 +773,128 @@ def fp4attn_norm_gate_backward(dz: torch.Tensor, dy: Optional[torch.Tensor], y: 
     return dict(dx=dx, dh=dh, dshift=dshift, dscale=dscale, dgate=dgate, dpre_weight=dpre, dpost_weight=dpost)
 
 
+# ------------------------------------------------------ differentiable --
+
+def _refuse_capture(name: str):
+    """The differentiable forms read the device status on the host, which a
+    graph capture cannot; the fp4attn_* calls under them can be captured."""
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError(f"{name} cannot be captured into a CUDA graph (it reads the device status on the host); "
+                           "capture the fp4attn_* calls instead")
+
+
+def _raise_status(workspace: torch.Tensor, where: str):
+    st = fp4attn_read_status(workspace)
+    if st != OK:
+        raise Fp4AttnError(st, where + " (device)")
+
+
+def _aligned_rows(t: torch.Tensor, unit: int = 8) -> torch.Tensor:
+    """t [rows, cols] itself, or a copy, with contiguous rows that start on 16 bytes."""
+    if (t.shape[1] <= 1 or t.stride(1) == 1) and t.data_ptr() % 16 == 0 and \
+            (t.shape[0] <= 1 or (t.stride(0) >= t.shape[1] and t.stride(0) % unit == 0)):
+        return t
+    rows, cols = t.shape
+    out = t.new_empty((rows, -(-cols // unit) * unit))[:, :cols]
+    return out.copy_(t)
+
+
+class FP4LinearSTE(torch.autograd.Function):
+    """Training-time NVFP4 linear layer: input and weight quantised under their
+    computed scales, straight-through backward."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias):
+        _refuse_capture("FP4LinearSTE")
+        K = weight.shape[1]
+        rows = _aligned_rows(x.reshape(-1, K))
+        w = _aligned_rows(weight, 4 if weight.dtype is torch.float32 else 8)
+        ws = new_linear_workspace(0, 0, 32, x.device)
+        qx = fp4attn_quantize_rows(rows, dynamic_gscale=True, workspace=ws)
+        qw = fp4attn_quantize_rows(w, dynamic_gscale=True, workspace=ws)
+        y = fp4attn_gemm(qx["codes"], qx["scales"], qw["codes"], qw["scales"], qx["gscale"], qw["gscale"],
+                         None if bias is None else bias.to(torch.bfloat16).contiguous(), workspace=ws)
+        _raise_status(ws, "FP4LinearSTE.forward")
+        ctx.save_for_backward(qx["codes"], qx["scales"], qx["gscale"], qw["codes"], qw["scales"], qw["gscale"])
+        ctx.x_shape, ctx.w_dtype, ctx.b_dtype = x.shape, weight.dtype, None if bias is None else bias.dtype
+        return y.view(*x.shape[:-1], weight.shape[0])
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        _refuse_capture("FP4LinearSTE")
+        xc, xs, gx, wc, wsc, gw = ctx.saved_tensors
+        rows = _aligned_rows(dy.to(torch.bfloat16).reshape(-1, wc.shape[0]))
+        ws = new_linear_backward_workspace(xc.shape[0], wc.shape[0], 2 * wc.shape[1], dy.device)
+        dx, dw, db = fp4attn_linear_backward(rows, xc, xs, wc, wsc, gx, gw, want_dx=ctx.needs_input_grad[0],
+                                             want_dw=ctx.needs_input_grad[1], want_dbias=ctx.needs_input_grad[2],
+                                             workspace=ws)
+        _raise_status(ws, "FP4LinearSTE.backward")
+        return (None if dx is None else dx.view(ctx.x_shape), None if dw is None else dw.to(ctx.w_dtype),
+                None if db is None else db.to(ctx.b_dtype))
+
+
+def fp4_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Differentiable NVFP4 linear layer of bf16 x [..., K] with a bf16 or fp32
+    weight [N, K] (fake quantisation of both under their computed scales, a
+    straight-through backward); K a multiple of 32.  The training-time
+    counterpart of fp4attn_linear, next to fp4_attention."""
+    assert x.dtype is torch.bfloat16 and weight.dim() == 2 and x.shape[-1] == weight.shape[1], "x [..., K], weight [N, K]"
+    return FP4LinearSTE.apply(x, weight, bias)
+
+
+class NormGate(torch.autograd.Function):
+    """fp4attn_norm_gate with fp4attn_norm_gate_backward as its gradient."""
+
+    @staticmethod
+    def forward(ctx, x, h, post_weight, gate, pre_weight, scale, shift, eps, flags, groups):
+        _refuse_capture("NormGate")
+        ctx.set_materialize_grads(False)
+        C = x.shape[-1]
+        unit = 4 if x.dtype is torch.float32 else 8
+        xr = _aligned_rows(x.reshape(-1, C), unit)
+        hr = None if h is None else _aligned_rows(h.reshape(-1, C))
+        vec = [None if t is None else _aligned_rows(t.reshape(-1, C)) for t in (gate, scale, shift)]
+        one = [None if t is None else t.contiguous() for t in (post_weight, pre_weight)]
+        ws = new_linear_workspace(0, 0, 32, x.device)
+        out = fp4attn_norm_gate(xr, hr, one[0], vec[0], one[1], vec[1], vec[2], eps=eps, flags=flags, groups=groups,
+                                workspace=ws)
+        _raise_status(ws, "NormGate.forward")
+        ctx.save_for_backward(out["y"], hr, one[0], vec[0], one[1], vec[1])
+        ctx.args = (eps, flags, groups if groups is not None else next((t.shape[0] for t in vec if t is not None), 1))
+        ctx.like = tuple(None if t is None else (t.shape, t.dtype) for t in (x, h, post_weight, gate, pre_weight, scale, shift))
+        return out["y"].view(x.shape), out["z"].view(x.shape)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dz):
+        _refuse_capture("NormGate")
+        y, h, post_weight, gate, pre_weight, scale = ctx.saved_tensors
+        eps, flags, groups = ctx.args
+        dzr = torch.zeros(y.shape, dtype=torch.bfloat16, device=y.device) if dz is None else \
+            _aligned_rows(dz.to(torch.bfloat16).reshape(y.shape))
+        dyr = None if dy is None else _aligned_rows(dy.to(y.dtype).reshape(y.shape), 4 if y.dtype is torch.float32 else 8)
+        ws = new_norm_backward_workspace(*y.shape, groups, device=y.device)
+        g = fp4attn_norm_gate_backward(dzr, dyr, y, h, post_weight, gate, pre_weight, scale, eps=eps, flags=flags,
+                                       groups=groups, workspace=ws)
+        _raise_status(ws, "NormGate.backward")
+        names = ("dx", "dh", "dpost_weight", "dgate", "dpre_weight", "dscale", "dshift")
+        grads = [None if like is None else g[k].to(like[1]).reshape(like[0]) for k, like in zip(names, ctx.like)]
+        # without a branch the gate and the branch's weight have no part in the result
+        return (*grads, None, None, None)
+
+
+def norm_gate(x: torch.Tensor, h: Optional[torch.Tensor] = None, post_weight: Optional[torch.Tensor] = None,
+              gate: Optional[torch.Tensor] = None, pre_weight: Optional[torch.Tensor] = None,
+              scale: Optional[torch.Tensor] = None, shift: Optional[torch.Tensor] = None, eps: float = 1e-6,
+              layer_norm: bool = False, groups: Optional[int] = None):
+    """Differentiable (y, z) of fp4attn_norm_gate for x [..., C] and h of x's
+    shape; the rows are `groups` equal samples one after the other (as many as
+    gate, scale and shift [groups, C] have)."""
+    assert h is not None or (gate is None and post_weight is None), "gate and post_weight belong to a branch h"
+    return NormGate.apply(x, h, post_weight, gate, pre_weight, scale, shift, eps, LAYER_NORM if layer_norm else 0, groups)
+
+
 def fp4attn_read_status(workspace: torch.Tensor, stream=None) -> int:
     v = ctypes.c_int(-1)
     _check(lib.fp4attn_read_status(_ptr(workspace), _stream(stream), ctypes.byref(v)), "fp4attn_read_status")

@@ -1,0 +1,268 @@
+"""The operators around the attention as they are used together: a block of
+quantised QKV projection, FP4 attention, output projection and gated norms, its
+training step, and the differentiable forms against 64-bit references."""
+import pytest
+import torch
+
+import linear_ref as ref
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+def _fa():
+    from nvfp4_precision_b200 import fp4attn
+    return fp4attn
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _randn(gen, *shape, std=1.0, dtype=BF):
+    return (std * torch.randn(*shape, generator=gen, device="cuda")).to(dtype)
+
+
+def _values(fa, q):
+    return fa.fp4attn_dequant_rows(q["codes"], q["scales"], q["gscale"], dtype=torch.float32).double()
+
+
+@pytest.mark.parametrize("lead,K,N", [((7,), 96, 40), ((2, 33), 256, 513), ((300,), 544, 200)])
+@pytest.mark.parametrize("wdtype", [BF, torch.float32])
+@pytest.mark.parametrize("bias", [False, True])
+def test_fp4_linear_and_its_gradients(lead, K, N, wdtype, bias):
+    fa = _fa()
+    gen = _gen(K + N)
+    x = _randn(gen, *lead, K).requires_grad_()
+    w = _randn(gen, N, K, std=K ** -0.5, dtype=wdtype).requires_grad_()
+    b = _randn(gen, N).requires_grad_() if bias else None
+    dy = _randn(gen, *lead, N)
+    y = fa.fp4_linear(x, w, b)
+    y.backward(dy)
+    xv = _values(fa, fa.fp4attn_quantize_rows(x.detach().view(-1, K), dynamic_gscale=True))
+    wv = _values(fa, fa.fp4attn_quantize_rows(w.detach(), dynamic_gscale=True))
+    g = dy.double().view(-1, N)
+
+    def check(got, a, c, add=None):
+        # the values are fl(fl(g s) e): two roundings each beside the exact products', then the fp32 sums
+        want, mag = a @ c, a.abs() @ c.abs()
+        if add is not None:
+            want, mag = want + add, mag + add.abs()
+        assert ref.worst(got, want, mag * (a.shape[1] + 24) * 2.0 ** -23) <= 1.0
+
+    check(y.detach().view(-1, N), xv, wv.t(), b.detach().double() if bias else None)
+    check(x.grad.view(-1, K), g, wv)
+    # a bf16 gradient, widened where the weight is fp32
+    check(w.grad.to(BF) if wdtype == torch.float32 else w.grad, g.t(), xv)
+    assert torch.equal(w.grad, w.grad.to(BF).to(wdtype))
+    if bias:
+        assert ref.worst(b.grad, g.sum(0), g.abs().sum(0) * g.shape[0] * ref.U) <= 1.0
+
+
+def test_fp4_linear_takes_views_and_skips_what_is_not_needed():
+    fa = _fa()
+    gen = _gen(2)
+    big = _randn(gen, 5, 40, 128)
+    x = big[:, ::2, :96]  # strided rows
+    w = _randn(gen, 72, 96, std=0.1).requires_grad_()
+    y = fa.fp4_linear(x, w)
+    assert torch.equal(y, fa.fp4_linear(x.contiguous(), w))
+    y.sum().backward()
+    assert w.grad is not None and big.grad is None
+    with torch.no_grad():
+        assert torch.equal(fa.fp4_linear(x, w), y)
+
+
+@pytest.mark.parametrize("layer", [False, True])
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_norm_gate_autograd(layer, dtype):
+    fa = _fa()
+    gen = _gen(4)
+    B, n, C = 3, 21, 200
+    x = _randn(gen, B, n, C, std=2.0, dtype=dtype).requires_grad_()
+    h = _randn(gen, B, n, C).requires_grad_()
+    mod = _randn(gen, B, 3 * C, std=0.3).requires_grad_()
+    w = [(1 + _randn(gen, C, std=0.1, dtype=torch.float32)).to(BF).requires_grad_() for _ in range(2)]
+    gate, scale, shift = mod.chunk(3, 1)
+    y, z = fa.norm_gate(x, h, w[0], gate, w[1], scale, shift, eps=1e-6, layer_norm=layer)
+    dy, dz = _randn(gen, B, n, C, dtype=dtype), _randn(gen, B, n, C)
+    torch.autograd.backward([y, z], [dy, dz])
+    two = lambda t: t.detach().reshape(B * n, C)
+    v = [t.detach() for t in (gate, scale, shift)]
+    want, bound = ref.norm_gate64(two(x), two(h), w[0].detach(), v[0], w[1].detach(), v[1], v[2], B, layer, 1e-6)
+    assert ref.worst(two(y), want["y"], bound["y"]) <= 1.0 and ref.worst(two(z), want["z"], bound["z"]) <= 1.0
+    want, bound = ref.norm_gate_backward64(two(dz), two(dy), two(y), two(h), w[0].detach(), v[0], w[1].detach(), v[1], B,
+                                           layer, 1e-6)
+    got = dict(dx=two(x.grad), dh=two(h.grad), dpost_weight=w[0].grad, dpre_weight=w[1].grad)
+    got.update(zip(("dgate", "dscale", "dshift"), mod.grad.chunk(3, 1)))
+    for k in want:
+        assert ref.worst(got[k], want[k], bound[k]) <= 1.0, k
+
+
+def test_norm_gate_autograd_of_one_output():
+    fa = _fa()
+    gen = _gen(6)
+    x, h = _randn(gen, 9, 64).requires_grad_(), _randn(gen, 9, 64).requires_grad_()
+    y, z = fa.norm_gate(x, h)
+    (gz,) = torch.autograd.grad(z, h, torch.ones_like(z), retain_graph=True)
+    ref_out = fa.fp4attn_norm_gate_backward(torch.ones_like(z), None, y.detach(), h.detach())
+    assert torch.equal(gz, ref_out["dh"])
+    (gy,) = torch.autograd.grad(y, x, torch.ones_like(y))
+    assert torch.equal(gy, torch.ones_like(y))  # z not used: the residual passes dy on
+    a, b = fa.norm_gate(x.detach().requires_grad_())
+    assert torch.equal(a, x)
+
+
+def test_differentiable_forms_refuse_a_capture():
+    fa = _fa()
+    x = torch.randn(4, 64, device="cuda").to(BF)
+    w = torch.randn(8, 64, device="cuda").to(BF)
+    for call in (lambda: fa.fp4_linear(x, w), lambda: fa.norm_gate(x)):
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held = x + 1  # a capture with something in it
+            with pytest.raises(RuntimeError, match="captured"):
+                call()
+        graph.replay()
+        assert torch.equal(held, x + 1)
+
+
+def _block(fa, p, x, h, B, n, H, D):
+    """norm -> NVFP4 QKV -> FP4 attention -> NVFP4 output projection -> gated norm."""
+    C = H * D
+    a = fa.fp4attn_norm_gate(x, h, quantize=True, z_gscale=p["gz"], workspace=p["ws"], **p["norm"])
+    qkv = fa.fp4attn_gemm(a["z_codes"], a["z_scales"], *p["wqkv"], x_gscale=p["gz"], w_gscale=p["gqkv"], bias=p["bqkv"],
+                          workspace=p["ws"])
+    q, k, v = (t.view(B, n, H, D).transpose(1, 2) for t in qkv.chunk(3, 1))
+    packed = fa.fp4attn_quantize_qk(q, k, workspace=p["aws"])
+    o, _ = fa.fp4attn_forward(packed["q_codes"], packed["q_scales"], packed["k_codes"], packed["k_scales"], v,
+                              o=p["o"].view(B, n, H, D).transpose(1, 2), workspace=p["aws"])
+    out = fa.fp4attn_linear(p["o"], *p["wo"], w_gscale=p["go"], dynamic_gscale=True, workspace=p["ws"])
+    return a["y"], qkv, out, fa.fp4attn_norm_gate(a["y"], out, workspace=p["ws"], **p["norm"])
+
+
+def test_a_block_end_to_end_and_replayed():
+    fa = _fa()
+    B, n, H, D = 2, 150, 2, 128
+    C, M = H * D, B * n
+    gen = _gen(9)
+    mod = _randn(gen, B, 3 * C, std=0.3)
+    gate, scale, shift = mod.chunk(3, 1)
+    ones = torch.ones(C, device="cuda").to(BF)
+    p = dict(norm=dict(post_weight=ones, gate=gate, pre_weight=ones, scale=scale, shift=shift),
+             gz=torch.tensor([0.01], device="cuda"), bqkv=_randn(gen, 3 * C), ws=fa.new_linear_workspace(M, 3 * C, C),
+             aws=fa.new_workspace(B, H, n), o=torch.empty(M, C, dtype=BF, device="cuda"))
+    for name, N in (("qkv", 3 * C), ("o", C)):
+        q = fa.fp4attn_quantize_rows(_randn(gen, N, C, std=C ** -0.5), dynamic_gscale=True)
+        p["w" + name], p["g" + name] = (q["codes"], q["scales"]), q["gscale"]
+    x, h = _randn(gen, M, C, std=2.0, dtype=torch.float32), _randn(gen, M, C)
+    y, qkv, out, last = _block(fa, p, x, h, B, n, H, D)
+    assert fa.fp4attn_read_status(p["ws"]) == 0 and fa.fp4attn_read_status(p["aws"]) == 0
+    # each step against its reference on the inputs that it had
+    nrm = (p["norm"][k] for k in ("post_weight", "gate", "pre_weight", "scale", "shift"))
+    nrm = list(nrm)
+    want, bound = ref.norm_gate64(x, h, *nrm, B, False, 1e-6)
+    assert ref.worst(y, want["y"], bound["y"]) <= 1.0
+    z = fa.fp4attn_norm_gate(x, h, **p["norm"])["z"]
+    zq = fa.fp4attn_quantize_rows(z, gscale=p["gz"])
+    zv, wv = _values(fa, zq), fa.fp4attn_dequant_rows(*p["wqkv"], p["gqkv"], dtype=torch.float32).double()
+    want, mag = zv @ wv.t() + p["bqkv"].double(), zv.abs() @ wv.abs().t() + p["bqkv"].double().abs()
+    assert ref.worst(qkv, want, mag * (C + 24) * 2.0 ** -23) <= 1.0
+    ov = _values(fa, fa.fp4attn_quantize_rows(p["o"], dynamic_gscale=True))
+    wv = fa.fp4attn_dequant_rows(*p["wo"], p["go"], dtype=torch.float32).double()
+    assert ref.worst(out, ov @ wv.t(), (ov.abs() @ wv.abs().t()) * (C + 24) * 2.0 ** -23) <= 1.0
+    want, bound = ref.norm_gate64(y, out, *nrm, B, False, 1e-6)
+    assert ref.worst(last["y"], want["y"], bound["y"]) <= 1.0 and ref.worst(last["z"], want["z"], bound["z"]) <= 1.0
+    # the whole chain captured once and replayed on other inputs
+    first = [t.clone() for t in (y, qkv, out, last["y"], last["z"])]
+    xs, hs = x.clone(), h.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ry, rqkv, rout, rlast = _block(fa, p, xs, hs, B, n, H, D)
+    for a, b in ((-x, -h), (x, h)):
+        xs.copy_(a)
+        hs.copy_(b)
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, (ry, rqkv, rout, rlast["y"], rlast["z"])))
+    assert fa.fp4attn_read_status(p["ws"]) == 0
+
+
+def test_a_training_step_has_gradients():
+    """Differentiable norm, projections and attention in one graph: finite gradients of every leaf, the same twice."""
+    fa = _fa()
+    B, n, H, D = 1, 130, 2, 128
+    C = H * D
+
+    def step():
+        gen = _gen(12)
+        x, h = (_randn(gen, B, n, C).requires_grad_() for _ in range(2))
+        wqkv, wo = (_randn(gen, N, C, std=C ** -0.5, dtype=torch.float32).requires_grad_() for N in (3 * C, C))
+        mod = _randn(gen, B, 3 * C, std=0.3).requires_grad_()
+        gate, scale, shift = mod.chunk(3, 1)
+        y, z = fa.norm_gate(x, h, None, gate, None, scale, shift)
+        q, k, v = (t.view(B, n, H, D).transpose(1, 2) for t in fa.fp4_linear(z, wqkv).chunk(3, -1))
+        o = fa.fp4_attention(q, k, v).transpose(1, 2).reshape(B, n, C)
+        y2, z2 = fa.norm_gate(y, fa.fp4_linear(o, wo))
+        (y2.float().square().mean() + z2.float().mean()).backward()
+        return [t.grad for t in (x, h, wqkv, wo, mod)]
+
+    a, b = step(), step()
+    for p, q in zip(a, b):
+        assert torch.isfinite(p).all() and p.abs().sum() > 0
+    # the attention's gradient of K passes through sums whose order may vary; the rest of the chain does not
+    assert torch.equal(a[3], b[3])
+
+
+def test_two_streams_with_a_workspace_each():
+    fa = _fa()
+    gen = _gen(14)
+    K, N = 544, 264
+    w = fa.fp4attn_quantize_rows(_randn(gen, N, K, std=0.05), dynamic_gscale=True)
+    xs = [_randn(gen, 300 + i, K) for i in range(2)]
+    want = [fa.fp4attn_linear(x, w["codes"], w["scales"], w["gscale"], dynamic_gscale=True) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    ws = [fa.new_linear_workspace(x.shape[0], N, K) for x in xs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            got[i].append(fa.fp4attn_linear(xs[i], w["codes"], w["scales"], w["gscale"], dynamic_gscale=True,
+                                            workspace=ws[i], stream=s))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g, want[i]) for g in got[i]) and fa.fp4attn_read_status(ws[i]) == 0
+
+
+def test_weights_quantised_right_before_they_are_used():
+    """Back to back on one stream, with launches that overlap: no kernel reads what the one before still writes."""
+    fa = _fa()
+    gen = _gen(15)
+    K, N, M = 2048, 1536, 64
+    x = fa.fp4attn_quantize_rows(_randn(gen, M, K))
+    xb = _randn(gen, M, K)
+    ws = fa.new_linear_workspace(M, N, K)
+    master = [_randn(gen, N, K, std=0.02, dtype=torch.float32) for _ in range(4)]
+    packed = [fa.fp4attn_quantize_rows(m, dynamic_gscale=True) for m in master]
+    torch.cuda.synchronize()
+    want = []
+    for q in packed:
+        want.append((fa.fp4attn_gemm(x["codes"], x["scales"], q["codes"], q["scales"], w_gscale=q["gscale"], workspace=ws),
+                     fa.fp4attn_linear(xb, q["codes"], q["scales"], q["gscale"], workspace=ws)))
+        torch.cuda.synchronize()
+    codes, scales = torch.empty_like(packed[0]["codes"]), torch.empty_like(packed[0]["scales"])
+    g = torch.empty(1, device="cuda")
+    for _ in range(10):
+        got = []
+        for m in master:
+            fa.fp4attn_quantize_rows(m, gscale=g, dynamic_gscale=True, codes=codes, scales=scales, workspace=ws)
+            a = fa.fp4attn_gemm(x["codes"], x["scales"], codes, scales, w_gscale=g, workspace=ws)
+            got.append((a, fa.fp4attn_linear(xb, codes, scales, g, workspace=ws)))
+        torch.cuda.synchronize()
+        for (a, b), (p, q) in zip(got, want):
+            assert torch.equal(a, p) and torch.equal(b, q)
+    assert fa.fp4attn_read_status(ws) == 0
