@@ -10,12 +10,11 @@
 // Both directions are bound by HBM: every row is read once and written once.
 // What it takes to get there is few instructions per value and enough bytes on
 // their way at any time:
-//   * A team of threads holds a row in registers, up to 24 values a thread, and
-//     walks down a range of rows of one sample after another.  Products of the
-//     per-channel vectors (gate post_weight, pre_weight (1 + scale), shift) are
-//     made once per sample and stay in registers, as the backward's sums down
-//     the columns do; hence one CTA of 256 threads and 255 registers per SM.
-//     Rows wider than 256 * 24 channels are shared by a cluster.
+//   * A team of warps holds a row in registers, up to 24 values a thread; the teams of a CTA (one per SM) take turns down a range of
+//     rows.  Products of the per-channel vectors (gate post_weight, pre_weight (1
+//     + scale), shift) are made once per range and sample, in shared memory; the
+//     backward's sums down the columns stay in registers over the range.  Rows
+//     too wide for a CTA are shared by a cluster.
 //   * The rows ahead come in by bulk copies into a ring in shared memory, one
 //     ring per team, so loads stay in flight through reductions and stores.
 //   * Two reductions over the team per row, for the layer norm too: its
@@ -38,12 +37,12 @@ namespace fp4attn {
 
 namespace {
 
-constexpr int NTHREADS = 256;
-constexpr int MAX_VALUES = 24;  // of a row, per thread
+constexpr int MAX_COLS = 6144;  // of a CTA
+constexpr int FWD_THREADS = 512;
 constexpr uint64_t kLimitNs = 2000000000ull;  // 2 s: far beyond any legitimate wait
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr int MAX_SLOTS = 6;
-constexpr int MAX_CLUSTER = 4;
+constexpr int MAX_CLUSTER = 3;  // 16384 channels
 
 // ---------------------------------------------------------------- teams --
 
@@ -87,22 +86,37 @@ __device__ __forceinline__ void load_vector(const __nv_bfloat16* p, int64_t at, 
     }
 }
 
-// What a thread knows of its team: TPR threads of the CTA, or (WIDE) the CTAs
-// of the cluster together.
-template <int TPR, bool WIDE>
+// What a thread knows of its team: TPR threads of the CTA, or (WIDE) of each CTA of
+// the cluster.  Sums of up to MAX_K quantities.  A wide team's warps write their
+// sums into every CTA and arrive on a barrier there: several teams of a cluster
+// go their own ways, and a row costs no barrier over all of it.
+template <int TPR, int MAX_K, bool WIDE>
 struct Team {
-    static constexpr int W = TPR / 32;
-    static constexpr int MAX_PARTS = W * (WIDE ? MAX_CLUSTER : 1);
-    static constexpr int MAX_K = 6;
-    static constexpr int SCRATCH = 2 * MAX_K * MAX_PARTS;  // floats per team: two buffers that alternate
+    static constexpr int warps = TPR / 32;
+    static constexpr int MAX_WARPS = (warps + 3) / 4 * 4 * (WIDE ? MAX_CLUSTER : 1);
+    // floats per team, zeroed: two buffers that alternate
+    static constexpr int SCRATCH = warps == 1 && !WIDE ? 4 : 2 * MAX_K * MAX_WARPS;
     float* scratch;
     int index, phase;
     uint32_t rank, ranks;
+    // WIDE: this team's barrier (ranks * warps arrivals), and what a wait needs
+    uint32_t bar, parity;
+    volatile int* abort_flag;
+    int* status;
 
-    __device__ __forceinline__ void sync() const {
+    // WIDE, behind the lanes' remote stores
+    __device__ __forceinline__ void arrive_and_wait() {
+        __syncwarp();
+        const int lane = threadIdx.x & 31;
+        if (lane < (int)ranks) mbar_arrive_cluster(mapa(bar, (uint32_t)lane));
+        mbar_wait_cluster(bar, parity, abort_flag, status, kLimitNs);
+        parity ^= 1;
+    }
+
+    __device__ __forceinline__ void sync() {
         if constexpr (WIDE)
-            cluster_sync();
-        else if constexpr (TPR == 32)
+            arrive_and_wait();
+        else if constexpr (warps == 1)
             __syncwarp();
         else
             asm volatile("bar.sync %0, %1;" ::"r"(1 + index), "n"(TPR) : "memory");
@@ -112,44 +126,39 @@ struct Team {
     // Ends every use that the threads made of shared memory before it.
     template <int K>
     __device__ __forceinline__ void sum(float (&v)[K]) {
+        static_assert(K <= MAX_K, "scratch");
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
             for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-        if constexpr (W == 1 && !WIDE) {
+        if constexpr (!WIDE && warps == 1) {
             __syncwarp();
         } else {
-            float* at = scratch + phase * (MAX_K * MAX_PARTS);
+            float* at = scratch + phase * (MAX_K * MAX_WARPS);
             phase ^= 1;
             const int warp = (threadIdx.x % TPR) >> 5, lane = threadIdx.x & 31;
             if constexpr (WIDE) {
                 if (lane < (int)ranks) {
                     const uint32_t base = mapa(smem_u32(at), (uint32_t)lane);
 #pragma unroll
-                    for (int k = 0; k < K; ++k) st_cluster(base + 4u * (k * MAX_PARTS + rank * W + warp), v[k]);
+                    for (int k = 0; k < K; ++k) st_cluster(base + 4u * (k * MAX_WARPS + rank * warps + warp), v[k]);
                 }
             } else if (lane == 0) {
 #pragma unroll
-                for (int k = 0; k < K; ++k) at[k * MAX_PARTS + warp] = v[k];
+                for (int k = 0; k < K; ++k) at[k * MAX_WARPS + warp] = v[k];
             }
             sync();
+            // what lies past the last warp is zero
+            const int n = WIDE ? warps * (int)ranks : MAX_WARPS;
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                float s = 0.0f;
-                if constexpr (WIDE) {
-                    for (int w = 0; w < (int)ranks * W; ++w) s += at[k * MAX_PARTS + w];
-                } else if constexpr (W >= 4) {
+            for (int k = 0; k < K; ++k) v[k] = 0.0f;
 #pragma unroll
-                    for (int w = 0; w < W; w += 4) {
-                        const float4 f = *reinterpret_cast<const float4*>(at + k * MAX_PARTS + w);
-                        s += (f.x + f.y) + (f.z + f.w);
-                    }
-                } else {
+            for (int w = 0; w < (WIDE ? n : MAX_WARPS); w += 4)
 #pragma unroll
-                    for (int w = 0; w < W; ++w) s += at[k * MAX_PARTS + w];
+                for (int k = 0; k < K; ++k) {
+                    const float4 f = *reinterpret_cast<const float4*>(at + k * MAX_WARPS + w);
+                    v[k] += (f.x + f.y) + (f.z + f.w);
                 }
-                v[k] = s;
-            }
         }
     }
 };
@@ -181,8 +190,8 @@ __device__ __forceinline__ float pivot_of(const void* row, int units) {
     return 0.125f * (s.x + s.y);
 }
 // The same pivot for every CTA of a cluster.
-template <int TPR, bool WIDE>
-__device__ __forceinline__ void share_pivots(Team<TPR, WIDE>& team, float& p, float& q) {
+template <int TPR, int MAX_K, bool WIDE>
+__device__ __forceinline__ void share_pivots(Team<TPR, MAX_K, WIDE>& team, float& p, float& q) {
     if constexpr (WIDE) {
         float v[2] = {threadIdx.x == 0 ? p : 0.0f, threadIdx.x == 0 ? q : 0.0f};
         team.sum(v);
@@ -199,15 +208,14 @@ __device__ __forceinline__ void share_pivots(Team<TPR, WIDE>& team, float& p, fl
 // registers for 512 threads, twice the warps of the backward to hide the
 // reductions and the quantiser behind.
 
-constexpr int FWD_THREADS = 512;
-
 template <int TPR, int J, int U, bool LAYER, bool QUANT, bool WIDE>
 __global__ void __launch_bounds__(FWD_THREADS, 1) norm_gate_kernel(const __grid_constant__ NormArgs a) {
-    constexpr int TEAMS = WIDE ? 1 : FWD_THREADS / TPR, ES = U == 4 ? 4 : 2, P = U / 2;
-    using TeamT = Team<TPR, WIDE>;
+    constexpr int TEAMS = FWD_THREADS / TPR, ES = U == 4 ? 4 : 2, P = U / 2;
+    using TeamT = Team<TPR, 2, WIDE>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t bars[TEAMS * MAX_SLOTS];
     __shared__ __align__(16) float scratch[TEAMS * TeamT::SCRATCH];
+    __shared__ uint64_t team_bars[TEAMS];
     __shared__ int abort_all;
     __shared__ ScaleTable table;  // not used (and not there) unless QUANT
     const int t = threadIdx.x % TPR;
@@ -217,13 +225,19 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) norm_gate_kernel(const __grid_
     team.phase = 0;
     team.rank = WIDE ? cluster_ctarank() : 0;
     team.ranks = WIDE ? cluster_nctarank() : 1;
+    team.bar = smem_u32(&team_bars[team.index]);
+    team.parity = 0;
+    team.abort_flag = &abort_all;
+    team.status = a.status;
     const int c0 = first_column(a.cols, team.rank), cols = min(a.cols, a.C - c0), NU = cols / U;
     pdl_wait();
     pdl_trigger();
     const float gz = QUANT ? (a.gz ? __ldg(a.gz) : 1.0f) : 1.0f;
     if (QUANT) make_scale_table(table, gz, threadIdx.x);
     if (threadIdx.x == 0) abort_all = 0;
-    if (threadIdx.x < TEAMS * MAX_SLOTS) mbar_init(smem_u32(&bars[threadIdx.x]), 1);
+    for (int i = threadIdx.x; i < TEAMS * MAX_SLOTS; i += blockDim.x) mbar_init(smem_u32(&bars[i]), 1);
+    for (int i = threadIdx.x; i < (int)(sizeof(scratch) / 4); i += blockDim.x) scratch[i] = 0.0f;
+    if (WIDE && threadIdx.x < TEAMS) mbar_init(smem_u32(&team_bars[threadIdx.x]), team.ranks * TeamT::warps);
     fence_mbar_init();
     __syncthreads();
     if constexpr (WIDE) cluster_sync();
@@ -495,6 +509,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) norm_gate_kernel(const __grid_
         for (int s = 0; s < a.slots; ++s)
             for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait(bars_u + 8u * s, ph, &dummy, nullptr, kDrainNs);
     }
+    if constexpr (WIDE) cluster_sync();  // no CTA leaves while another may write into it
 }
 
 // ------------------------------------------------------------ backward --
@@ -503,17 +518,21 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) norm_gate_kernel(const __grid_
 //   dx = dy + r (dn - n mean(dn n) - [layer] mean(dn))
 // and with m = norm(h), dm = dx gate post:
 //   dh = r_h (dm - m mean(dm m) - [layer] mean(dm))
-// Sums down the rows of a sample: dz, dz n, dx m.  A row is read from its slot
-// twice (y and dy need not stay in registers in between); the slot is filled
-// again one row later, behind the barrier that shows that everyone is done.
+// Sums down the rows of a sample: dz, dz n, dx m, in registers over a CTA's
+// range of rows of one sample (an item), then over its teams in order.  A row is
+// read from its slot twice (y and dy need not stay in registers in between).
 
-template <int TPR, int J, int U, bool LAYER, bool WIDE>
-__global__ void __launch_bounds__(NTHREADS, 1) norm_gate_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
-    constexpr int TEAMS = NTHREADS / TPR, ES = U == 4 ? 4 : 2, P = U / 2;
-    using TeamT = Team<TPR, WIDE>;
+template <int THREADS, int TPR, int J, int U, bool LAYER, bool WIDE>
+__global__ void __launch_bounds__(THREADS, 1) norm_gate_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
+    constexpr int TEAMS = THREADS / TPR, ES = U == 4 ? 4 : 2, P = U / 2;
+    // 255 registers hold the vectors as well: 36864 x 6144, bf16: 476 -> 452 us (fp32
+    // rows, whose loads take more of them: 625 -> 666)
+    constexpr bool HELD = THREADS == 256 && U == 8;
+    using TeamT = Team<TPR, 6, WIDE>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t bars[TEAMS * MAX_SLOTS];
     __shared__ __align__(16) float scratch[TEAMS * TeamT::SCRATCH];
+    __shared__ uint64_t team_bars[TEAMS];
     __shared__ int abort_all;
     const int t = threadIdx.x % TPR;
     TeamT team;
@@ -522,9 +541,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) norm_gate_bwd_kernel(const __grid
     team.phase = 0;
     team.rank = WIDE ? cluster_ctarank() : 0;
     team.ranks = WIDE ? cluster_nctarank() : 1;
+    team.bar = smem_u32(&team_bars[team.index]);
+    team.parity = 0;
+    team.abort_flag = &abort_all;
+    team.status = a.status;
     const int c0 = first_column(a.cols, team.rank), cols = min(a.cols, a.C - c0), NU = cols / U;
     if (threadIdx.x == 0) abort_all = 0;
-    if (threadIdx.x < TEAMS * MAX_SLOTS) mbar_init(smem_u32(&bars[threadIdx.x]), 1);
+    for (int i = threadIdx.x; i < TEAMS * MAX_SLOTS; i += blockDim.x) mbar_init(smem_u32(&bars[i]), 1);
+    for (int i = threadIdx.x; i < (int)(sizeof(scratch) / 4); i += blockDim.x) scratch[i] = 0.0f;
+    if (WIDE && threadIdx.x < TEAMS) mbar_init(smem_u32(&team_bars[threadIdx.x]), team.ranks * TeamT::warps);
     fence_mbar_init();
     __syncthreads();
     if constexpr (WIDE) cluster_sync();
@@ -537,61 +562,105 @@ __global__ void __launch_bounds__(NTHREADS, 1) norm_gate_bwd_kernel(const __grid
     // a slot: y, dy (residual type), dz, h (bf16)
     const uint32_t at_dy = res_bytes, at_dz = at_dy + (has_dy ? res_bytes : 0), at_h = at_dz + half_bytes;
     const uint32_t row_bytes = at_h + (has_h ? half_bytes : 0);
-    const uint8_t* ring = smem + (size_t)team.index * a.slots * a.slot_bytes;
+    // shared memory: A = gate post_weight and B = pre_weight (1 + scale), four
+    // channels an entry (see the forward); where teams meet; the rings
+    float4* vectors = reinterpret_cast<float4*>(smem);
+    const int plane = a.cols / U;
+    float* meet = reinterpret_cast<float*>(smem + (size_t)8 * a.cols);
+    const uint8_t* ring = smem + (size_t)(TEAMS > 1 ? 20 : 8) * a.cols + (size_t)team.index * a.slots * a.slot_bytes;
     const uint32_t ring_u = smem_u32(ring), bars_u = smem_u32(&bars[team.index * MAX_SLOTS]);
-    const int64_t teams = (int64_t)(gridDim.x / team.ranks) * TEAMS;
-    const int64_t id = blockIdx.x / team.ranks + (int64_t)(gridDim.x / team.ranks) * team.index;
+    const int64_t clusters = gridDim.x / team.ranks, first_item = blockIdx.x / team.ranks;
     const int64_t items = a.groups * a.parts;
     auto item_rows = [&](int64_t item, int64_t& begin, int64_t& end) {
         const int64_t g = item / a.parts, p = item - g * a.parts;
         begin = g * a.rows_per_group + a.rows_per_group * p / a.parts;
         end = g * a.rows_per_group + a.rows_per_group * (p + 1) / a.parts;
     };
-    // the rows ahead, over the items of this team (an item has a row at least)
-    int64_t ahead_item = id, ahead = 0, ahead_end = 0;
-    if (ahead_item < items) item_rows(ahead_item, ahead, ahead_end);
+    // the rows ahead of this team, over its CTA's items
+    int64_t ahead_item = first_item, ahead = 0, ahead_end = 0;
+    auto seek = [&]() {  // from a new item on to one that has a row for this team
+        for (; ahead_item < items; ahead_item += clusters) {
+            item_rows(ahead_item, ahead, ahead_end);
+            ahead += team.index;
+            if (ahead < ahead_end) return;
+        }
+    };
     auto fill_next = [&](int slot) {  // by thread 0
         if (ahead_item >= items) return;
-        const int64_t row = ahead++;
         const uint32_t bar = bars_u + 8u * slot, at = ring_u + a.slot_bytes * slot;
         mbar_arrive_expect_tx(bar, row_bytes);
-        bulk_load(at, static_cast<const uint8_t*>(a.y) + (row * a.ldy + c0) * ES, res_bytes, bar);
-        if (has_dy) bulk_load(at + at_dy, static_cast<const uint8_t*>(a.dy) + (row * a.lddy + c0) * ES, res_bytes, bar);
-        bulk_load(at + at_dz, a.dz + row * a.lddz + c0, half_bytes, bar);
-        if (has_h) bulk_load(at + at_h, a.h + row * a.ldh + c0, half_bytes, bar);
-        if (ahead >= ahead_end && (ahead_item += teams) < items) item_rows(ahead_item, ahead, ahead_end);
+        bulk_load(at, static_cast<const uint8_t*>(a.y) + (ahead * a.ldy + c0) * ES, res_bytes, bar);
+        if (has_dy) bulk_load(at + at_dy, static_cast<const uint8_t*>(a.dy) + (ahead * a.lddy + c0) * ES, res_bytes, bar);
+        bulk_load(at + at_dz, a.dz + ahead * a.lddz + c0, half_bytes, bar);
+        if (has_h) bulk_load(at + at_h, a.h + ahead * a.ldh + c0, half_bytes, bar);
+        ahead += TEAMS;
+        if (ahead >= ahead_end) {
+            ahead_item += clusters;
+            seek();
+        }
     };
-    if (t == 0)
+    if (t == 0) {
+        seek();
         for (int s = 0; s < a.slots; ++s) fill_next(s);
+    }
     const float inv_c = 1.0f / (float)a.C;
-    int slot = 0, done = -1;  // done: the slot of the row before
+    int slot = 0;
     uint32_t parity = 0;
-    for (int64_t item = id; item < items; item += teams) {
+    auto vector = [&](int which, int u, float2(&v)[P]) {
+#pragma unroll
+        for (int k = 0; k < U / 4; ++k) {
+            const float4 f = vectors[(which * (U / 4) + k) * plane + u];
+            v[2 * k] = make_float2(f.x, f.y);
+            v[2 * k + 1] = make_float2(f.z, f.w);
+        }
+    };
+    for (int64_t item = first_item; item < items; item += clusters) {
         int64_t begin, end;
         item_rows(item, begin, end);
         const int64_t group = item / a.parts;
-        float2 A[J][P], B[J][P], s_dz[J][P], s_dzn[J][P], s_dxm[J][P];
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int u = t + TPR * j;
-            const bool on = u < NU;
-            const int64_t c = on ? c0 + U * u : 0;
+        __syncthreads();
+        for (int u = threadIdx.x; u < NU; u += blockDim.x) {
+            const int64_t c = c0 + U * u;
             float2 p[P], q[P];
+            auto put = [&](int which) {
+#pragma unroll
+                for (int k = 0; k < U / 4; ++k)
+                    vectors[(which * (U / 4) + k) * plane + u] = make_float4(p[2 * k].x, p[2 * k].y, p[2 * k + 1].x, p[2 * k + 1].y);
+            };
             load_vector<U>(a.gate, group * a.lgate + c, 1.0f, p);
             load_vector<U>(a.post, c, 1.0f, q);
 #pragma unroll
-            for (int i = 0; i < P; ++i) A[j][i] = on ? __fmul2_rn(p[i], q[i]) : both(0.0f);
+            for (int i = 0; i < P; ++i) p[i] = __fmul2_rn(p[i], q[i]);
+            put(0);
             load_vector<U>(a.pre, c, 1.0f, p);
             load_vector<U>(a.scale, group * a.lscale + c, 0.0f, q);
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                B[j][i] = on ? __ffma2_rn(p[i], q[i], p[i]) : both(0.0f);
-                s_dz[j][i] = s_dzn[j][i] = s_dxm[j][i] = both(0.0f);
+            for (int i = 0; i < P; ++i) p[i] = __ffma2_rn(p[i], q[i], p[i]);
+            put(1);
+        }
+        __syncthreads();
+        float2 s_dz[J][P], s_dzn[J][P], s_dxm[J][P], held_A[J][P], held_B[J][P];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) s_dz[j][i] = s_dzn[j][i] = s_dxm[j][i] = both(0.0f);
+            if (HELD) {
+                const int u = min(t + TPR * j, NU - 1);
+                vector(0, u, held_A[j]);
+                vector(1, u, held_B[j]);
             }
         }
-        uint8_t* dx_at = static_cast<uint8_t*>(a.dx) + (begin * a.lddx + c0) * ES;
-        __nv_bfloat16* dh_at = a.dh + (begin * a.lddh + c0);
-        for (int64_t row = begin; row < end; ++row, dx_at += a.lddx * ES, dh_at += a.lddh) {
+        auto gate_of = [&](int j, int u, float2(&v)[P]) {
+            if (!HELD) return vector(0, u, v);
+#pragma unroll
+            for (int i = 0; i < P; ++i) v[i] = held_A[j][i];
+        };
+        auto pre_of = [&](int j, int u, float2(&v)[P]) {
+            if (!HELD) return vector(1, u, v);
+#pragma unroll
+            for (int i = 0; i < P; ++i) v[i] = held_B[j][i];
+        };
+        for (int64_t row = begin + team.index; row < end; row += TEAMS) {
             const bool ok = mbar_wait(bars_u + 8u * slot, parity, abort_flag, a.status, kLimitNs);
             const uint8_t* at = ring + (size_t)a.slot_bytes * slot;
             Packed<U> dz[J], h[J];
@@ -612,25 +681,26 @@ __global__ void __launch_bounds__(NTHREADS, 1) norm_gate_bwd_kernel(const __grid
                 }
             }
             float ry, rh, mean_y = 0.0f, mean_h = 0.0f, mean_dn = 0.0f, c1;
-            for (int again = 0;; ++again) {
+            // sums about the pivots p of y and q of h; whether those were near enough
+            auto moments = [&]() -> bool {
                 float2 s_y = both(0.0f), s_y2 = both(0.0f), s_dn = both(0.0f), s_dny = both(0.0f), s_h = both(0.0f),
                        s_h2 = both(0.0f);
-                const float2 p2 = both(-p), q2 = both(-q);
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
                     const int u = t + TPR * j;
                     if (u < NU) {
-                        float2 y[P], d[P], f[P];
+                        float2 y[P], d[P], f[P], B[P];
                         load_res(at, u, y);
                         if (!ok) y[0].x = __int_as_float(0x7FC00000);  // a row that never came
                         unpack(dz[j], d);
                         unpack(h[j], f);
+                        pre_of(j, u, B);
 #pragma unroll
                         for (int i = 0; i < P; ++i) {
-                            d[i] = __fmul2_rn(d[i], B[j][i]);
+                            d[i] = __fmul2_rn(d[i], B[i]);
                             if constexpr (LAYER) {
-                                y[i] = __fadd2_rn(y[i], p2);
-                                f[i] = __fadd2_rn(f[i], q2);
+                                y[i] = __fadd2_rn(y[i], both(-p));
+                                f[i] = __fadd2_rn(f[i], both(-q));
                                 s_y = __fadd2_rn(s_y, y[i]);
                                 s_h = __fadd2_rn(s_h, f[i]);
                                 s_dn = __fadd2_rn(s_dn, d[i]);
@@ -647,7 +717,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) norm_gate_bwd_kernel(const __grid
                     ry = rsqrtf(__fmaf_rn(s[0], inv_c, a.eps));
                     rh = rsqrtf(__fmaf_rn(s[2], inv_c, a.eps));
                     c1 = s[1] * inv_c * ry;  // mean(dn n)
-                    break;
+                    return true;
                 } else {
                     float s[6] = {s_y.x + s_y.y, s_y2.x + s_y2.y, s_dn.x + s_dn.y, s_dny.x + s_dny.y, s_h.x + s_h.y,
                                   s_h2.x + s_h2.y};
@@ -660,27 +730,26 @@ __global__ void __launch_bounds__(NTHREADS, 1) norm_gate_bwd_kernel(const __grid
                     ry = rsqrtf(fmaxf(vy, 0.0f) + a.eps);
                     rh = rsqrtf(fmaxf(vh, 0.0f) + a.eps);
                     c1 = (s[3] * inv_c - d * mean_dn) * ry;
-                    if (again || (d * d <= vy && e * e <= vh)) break;
-                    p = mean_y;
-                    q = mean_h;
+                    return d * d <= vy && e * e <= vh;
                 }
+            };
+            if (!moments()) {
+                p = mean_y;
+                q = mean_h;
+                moments();
             }
-            // the row before has left its slot
-            if (t == 0 && done >= 0 && !*abort_flag) fill_next(done);
-            done = slot;
-            if (++slot == a.slots) {
-                slot = 0;
-                parity ^= 1;
-            }
+            // n = y r - mean r and the like: the products' roundings are of the size
+            // of the mean's own.  dx = dy + r dn - r c1 n - r mean(dn)
             float2 dm[J][P];
             float2 s_dmm = both(0.0f), s_dm = both(0.0f);
-            const float2 my2 = both(-mean_y), mh2 = both(-mean_h), ry2 = both(ry), rh2 = both(rh), c12 = both(-c1),
-                         md2 = both(-mean_dn);
+            const float2 ry2 = both(ry), rh2 = both(rh), my2 = both(-mean_y * ry), mh2 = both(-mean_h * rh),
+                         c12 = both(-c1 * ry), md2 = both(-mean_dn * ry);
+            uint8_t* dx_at = static_cast<uint8_t*>(a.dx) + (row * a.lddx + c0) * ES;
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const int u = t + TPR * j;
                 if (u < NU) {
-                    float2 y[P], d[P], f[P], g[P];
+                    float2 y[P], d[P], f[P], g[P], A[P], B[P];
                     load_res(at, u, y);
                     if (has_dy) {
                         load_res(at + at_dy, u, g);
@@ -690,38 +759,47 @@ __global__ void __launch_bounds__(NTHREADS, 1) norm_gate_bwd_kernel(const __grid
                     }
                     unpack(dz[j], d);
                     unpack(h[j], f);
+                    gate_of(j, u, A);
+                    pre_of(j, u, B);
 #pragma unroll
                     for (int i = 0; i < P; ++i) {
-                        if (LAYER) y[i] = __fadd2_rn(y[i], my2);
-                        const float2 n = __fmul2_rn(y[i], ry2);
+                        const float2 n = LAYER ? __ffma2_rn(y[i], ry2, my2) : __fmul2_rn(y[i], ry2);
+                        const float2 m = LAYER ? __ffma2_rn(f[i], rh2, mh2) : __fmul2_rn(f[i], rh2);
                         s_dz[j][i] = __fadd2_rn(s_dz[j][i], d[i]);
                         s_dzn[j][i] = __ffma2_rn(d[i], n, s_dzn[j][i]);
-                        float2 e = __ffma2_rn(n, c12, __fmul2_rn(d[i], B[j][i]));
-                        if (LAYER) e = __fadd2_rn(e, md2);
-                        g[i] = __ffma2_rn(e, ry2, g[i]);  // dx
-                        if (LAYER) f[i] = __fadd2_rn(f[i], mh2);
-                        const float2 m = __fmul2_rn(f[i], rh2);
+                        if (LAYER) g[i] = __fadd2_rn(g[i], md2);
+                        g[i] = __ffma2_rn(n, c12, g[i]);
+                        g[i] = __ffma2_rn(__fmul2_rn(d[i], B[i]), ry2, g[i]);  // dx
                         s_dxm[j][i] = __ffma2_rn(g[i], m, s_dxm[j][i]);
-                        dm[j][i] = __fmul2_rn(g[i], A[j][i]);
+                        dm[j][i] = __fmul2_rn(g[i], A[i]);
                         s_dmm = __ffma2_rn(dm[j][i], m, s_dmm);
                         if (LAYER) s_dm = __fadd2_rn(s_dm, dm[j][i]);
                     }
                     if (FP4ATTN_IN_BOUNDS(row < a.rows && c0 + U * u + U <= a.C, a.status)) store_res(dx_at, u, g);
                 }
             }
-            if (!has_h) continue;
-            float c2, mean_dm = 0.0f;
-            if constexpr (LAYER) {
+            float k1 = 0.0f, k0 = 0.0f;  // dh = r dm + k1 h + k0
+            if (!has_h) {
+                team.sync();
+            } else if constexpr (LAYER) {
                 float s[2] = {s_dmm.x + s_dmm.y, s_dm.x + s_dm.y};
                 team.sum(s);
-                c2 = s[0] * inv_c;
-                mean_dm = s[1] * inv_c;
+                k1 = -rh * rh * (s[0] * inv_c);
+                k0 = -k1 * mean_h - rh * (s[1] * inv_c);
             } else {
                 float s[1] = {s_dmm.x + s_dmm.y};
                 team.sum(s);
-                c2 = s[0] * inv_c;
+                k1 = -rh * rh * (s[0] * inv_c);
             }
-            const float2 c22 = both(-c2), mdm2 = both(-mean_dm);
+            // no thread reads the slot any more
+            if (t == 0 && !*abort_flag) fill_next(slot);
+            if (++slot == a.slots) {
+                slot = 0;
+                parity ^= 1;
+            }
+            if (!has_h) continue;
+            const float2 k12 = both(k1), k02 = both(k0);
+            __nv_bfloat16* dh_at = a.dh + (row * a.lddh + c0);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const int u = t + TPR * j;
@@ -729,33 +807,43 @@ __global__ void __launch_bounds__(NTHREADS, 1) norm_gate_bwd_kernel(const __grid
                     float2 f[P];
                     unpack(h[j], f);
 #pragma unroll
-                    for (int i = 0; i < P; ++i) {
-                        if (LAYER) f[i] = __fadd2_rn(f[i], mh2);
-                        float2 e = __ffma2_rn(__fmul2_rn(f[i], rh2), c22, dm[j][i]);
-                        if (LAYER) e = __fadd2_rn(e, mdm2);
-                        f[i] = __fmul2_rn(e, rh2);
-                    }
+                    for (int i = 0; i < P; ++i)
+                        f[i] = __ffma2_rn(dm[j][i], rh2, LAYER ? __ffma2_rn(f[i], k12, k02) : __fmul2_rn(f[i], k12));
                     if (FP4ATTN_IN_BOUNDS(row < a.rows && c0 + U * u + U <= a.C, a.status))
                         reinterpret_cast<Packed<U>*>(dh_at)[u] = pack(f);
                 }
             }
         }
+        // the teams' sums, one team after the other; the last one writes them out
         float* part = a.part + item * 3 * (int64_t)a.C + c0;
+        for (int k = 0; k < TEAMS; ++k) {
+            if (team.index == k) {
+                const bool last = k == TEAMS - 1;
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int u = t + TPR * j;
-            if (u < NU && FP4ATTN_IN_BOUNDS(item < items, a.status)) {
+                for (int j = 0; j < J; ++j) {
+                    const int u = t + TPR * j;
+                    if (u < NU && FP4ATTN_IN_BOUNDS(item < items, a.status)) {
 #pragma unroll
-                for (int i = 0; i < P; i += 2) {
-                    const int c = U * u + 2 * i;
-                    *reinterpret_cast<float4*>(part + c) =
-                        make_float4(s_dz[j][i].x, s_dz[j][i].y, s_dz[j][i + 1].x, s_dz[j][i + 1].y);
-                    *reinterpret_cast<float4*>(part + a.C + c) =
-                        make_float4(s_dzn[j][i].x, s_dzn[j][i].y, s_dzn[j][i + 1].x, s_dzn[j][i + 1].y);
-                    *reinterpret_cast<float4*>(part + 2 * (int64_t)a.C + c) =
-                        make_float4(s_dxm[j][i].x, s_dxm[j][i].y, s_dxm[j][i + 1].x, s_dxm[j][i + 1].y);
+                        for (int w = 0; w < 3; ++w) {
+                            const float2(&v)[P] = w == 0 ? s_dz[j] : w == 1 ? s_dzn[j] : s_dxm[j];
+#pragma unroll
+                            for (int i = 0; i < P; i += 2) {
+                                float4 f = make_float4(v[i].x, v[i].y, v[i + 1].x, v[i + 1].y);
+                                float4* const m = reinterpret_cast<float4*>(meet + w * cols + U * u + 2 * i);
+                                if (k > 0) {
+                                    const float4 o = *m;
+                                    f = make_float4(o.x + f.x, o.y + f.y, o.z + f.z, o.w + f.w);
+                                }
+                                if (last)
+                                    *reinterpret_cast<float4*>(part + w * (int64_t)a.C + U * u + 2 * i) = f;
+                                else
+                                    *m = f;
+                            }
+                        }
+                    }
                 }
             }
+            if (k < TEAMS - 1) __syncthreads();
         }
     }
     if (t == 0 && *abort_flag) {
@@ -763,6 +851,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) norm_gate_bwd_kernel(const __grid
         for (int s = 0; s < a.slots; ++s)
             for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait(bars_u + 8u * s, ph, &dummy, nullptr, kDrainNs);
     }
+    if constexpr (WIDE) cluster_sync();  // no CTA leaves while another may write into it
 }
 
 // Adds a sample's parts in order (32 columns by 8 shares of the parts per CTA;
@@ -840,25 +929,50 @@ __global__ void __launch_bounds__(256) norm_weights_kernel(const __grid_constant
     if (a.dpost) a.dpost[c] = s[1];
 }
 
-// Shared memory of the rings (and the forward's vectors).
-constexpr size_t RING_BYTES = 222 * 1024;
-// the backward fills a slot one row late: it needs two at its widest rows
-static_assert(2 * 12 * (size_t)NTHREADS * MAX_VALUES <= RING_BYTES, "two slots of the widest rows");
+constexpr size_t SMEM_BYTES = 221 * 1024;  // of the vectors and rings
+static_assert((8 + 2 * 12) * (size_t)MAX_COLS <= SMEM_BYTES && (20 + 4 * 12) * (size_t)(MAX_COLS / 2) <= SMEM_BYTES,
+              "two slots of the widest rows");
+static_assert((12 + 2 * 2 * 6) * (size_t)MAX_COLS <= SMEM_BYTES, "two slots of the forward's two widest teams");
 
-// How a row of C channels is shared out: CTAs of a cluster, threads of a CTA
-// per row, values per thread in eights.
+// How rows of C channels are shared out: CTAs of a cluster, channels, threads
+// and teams of a CTA, threads of a team, values a thread in eights.
 struct Split {
-    int ctas, cols, tpr, j8;
+    int ctas, cols, threads, teams, tpr, j8;
 };
-Split split_of(int64_t C) {
-    Split s{1, (int)C, NTHREADS, 0};
-    const int64_t most = NTHREADS * MAX_VALUES;
-    if (C > most) {
-        s.ctas = C > 2 * most ? MAX_CLUSTER : 2;
-        s.cols = (int)((C + 64 * s.ctas - 1) / (64 * s.ctas) * 64);
+void share_columns(Split& s, int64_t C) {
+    s.ctas = (int)((C + MAX_COLS - 1) / MAX_COLS);
+    s.cols = s.ctas == 1 ? (int)C : (int)((C + 64 * s.ctas - 1) / (64 * s.ctas) * 64);
+}
+// Forward: up to 24 values a thread, teams of 32 to 256.
+Split forward_split(int64_t C) {
+    Split s{};
+    share_columns(s, C);
+    for (s.tpr = s.ctas > 1 ? 256 : 32; s.tpr * 24 < s.cols;) s.tpr *= 2;
+    s.j8 = s.tpr == 32 || s.tpr == 256 ? (s.cols + 8 * s.tpr - 1) / (8 * s.tpr) : 3;
+    if (s.tpr == 256 && (s.j8 < 2 || s.ctas > 1)) s.j8 = s.ctas > 1 ? 3 : 2;
+    s.teams = FWD_THREADS / s.tpr;
+    s.threads = s.teams * s.tpr;
+    return s;
+}
+// Backward: narrow rows 16 values a thread and 384 threads of 168 registers,
+// wide ones 24 and 256 of 255.  100000 x 512: 121 us the first way, 138 the
+// second; 36864 x 6144, layer norm: 664 and 617.
+Split backward_split(int64_t C) {
+    Split s{};
+    share_columns(s, C);
+    if (s.ctas == 1 && s.cols <= 192 * 16) {
+        static const int teams_of[5] = {32, 64, 96, 128, 192};
+        int i = 0;
+        while (teams_of[i] * 16 < s.cols) ++i;
+        s.tpr = teams_of[i];
+        s.j8 = s.cols <= 256 ? 1 : 2;
+        s.threads = 384;
+        s.teams = s.threads / s.tpr;
+    } else {
+        s.tpr = s.threads = 256;
+        s.j8 = s.ctas == 1 && s.cols <= 256 * 16 ? 2 : 3;
+        s.teams = 1;
     }
-    while (s.tpr > 32 && s.cols <= s.tpr / 2 * MAX_VALUES) s.tpr /= 2;
-    s.j8 = (s.cols + 8 * s.tpr - 1) / (8 * s.tpr);
     return s;
 }
 
@@ -869,24 +983,40 @@ struct Shape {
     int slots;
     size_t smem;
 };
-int shape_of(const void* kernel, const Split& s, int teams, size_t fixed_bytes, size_t slot_bytes, int64_t work, Shape& sh) {
-    sh.slots = (int)((RING_BYTES - fixed_bytes) / (slot_bytes * teams));
+int shape_of(const void* kernel, const Split& s, size_t fixed_bytes, size_t slot_bytes, int64_t work, Shape& sh) {
+    sh.slots = (int)((SMEM_BYTES - fixed_bytes) / (slot_bytes * s.teams));
     sh.slots = sh.slots < 1 ? 1 : sh.slots > MAX_SLOTS ? MAX_SLOTS : sh.slots;
-    sh.smem = fixed_bytes + slot_bytes * teams * sh.slots;
+    sh.smem = fixed_bytes + slot_bytes * s.teams * sh.slots;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh.smem) != cudaSuccess)
         return FP4ATTN_ERR_CUDA;
     int64_t clusters = sms / s.ctas;
+    if (s.ctas > 1) {
+        // not every SM finds a place in a cluster: a launch of more would go in two turns
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)(clusters * s.ctas));
+        cfg.blockDim = dim3((unsigned)s.threads);
+        cfg.dynamicSmemBytes = sh.smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)s.ctas;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int fit = 0;
+        if (cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg) != cudaSuccess || fit < 1) return FP4ATTN_ERR_CUDA;
+        clusters = clusters < fit ? clusters : fit;
+    }
     clusters = clusters < work ? clusters : work;
     sh.grid = (unsigned)(clusters * s.ctas);
     return FP4ATTN_OK;
 }
 
 template <typename Args>
-int launch(void (*kernel)(Args), const Args& a, int threads, const Split& s, const Shape& sh, cudaStream_t stream) {
-    return launch_behind(kernel, dim3(sh.grid), (unsigned)threads, sh.smem, stream, (unsigned)s.ctas, a) == cudaSuccess
+int launch(void (*kernel)(Args), const Args& a, const Split& s, const Shape& sh, cudaStream_t stream) {
+    return launch_behind(kernel, dim3(sh.grid), (unsigned)s.threads, sh.smem, stream, (unsigned)s.ctas, a) == cudaSuccess
                ? FP4ATTN_OK
                : FP4ATTN_ERR_CUDA;
 }
@@ -904,50 +1034,66 @@ FwdKernel fwd_of(bool f32, bool layer, bool quant) {
     if (layer) return quant ? norm_gate_kernel<TPR, J8, 8, true, true, WIDE> : norm_gate_kernel<TPR, J8, 8, true, false, WIDE>;
     return quant ? norm_gate_kernel<TPR, J8, 8, false, true, WIDE> : norm_gate_kernel<TPR, J8, 8, false, false, WIDE>;
 }
-template <int TPR, int J8, bool WIDE>
-BwdKernel bwd_of(bool f32, bool layer, bool) {
-    if (f32) return layer ? norm_gate_bwd_kernel<TPR, 2 * J8, 4, true, WIDE> : norm_gate_bwd_kernel<TPR, 2 * J8, 4, false, WIDE>;
-    return layer ? norm_gate_bwd_kernel<TPR, J8, 8, true, WIDE> : norm_gate_bwd_kernel<TPR, J8, 8, false, WIDE>;
+FwdKernel forward_kernel(const Split& s, bool f32, bool layer, bool quant) {
+    if (s.ctas > 1) return fwd_of<256, 3, true>(f32, layer, quant);
+    switch (s.tpr) {
+        case 32:
+            return s.j8 == 1   ? fwd_of<32, 1, false>(f32, layer, quant)
+                   : s.j8 == 2 ? fwd_of<32, 2, false>(f32, layer, quant)
+                               : fwd_of<32, 3, false>(f32, layer, quant);
+        case 64: return fwd_of<64, 3, false>(f32, layer, quant);
+        case 128: return fwd_of<128, 3, false>(f32, layer, quant);
+    }
+    return s.j8 == 2 ? fwd_of<256, 2, false>(f32, layer, quant) : fwd_of<256, 3, false>(f32, layer, quant);
 }
-
-// Teams of 32 threads take 1 to 3 eights a thread, larger ones 2 or 3 (fewer
-// than that fits a team of half the size).
-#define FP4ATTN_NORM_KERNEL(of, s, f32, layer, quant)                                                                  \
-    ((s).ctas > 1    ? ((s).j8 <= 2 ? of<256, 2, true>(f32, layer, quant) : of<256, 3, true>(f32, layer, quant))       \
-     : (s).tpr == 32 ? ((s).j8 == 1   ? of<32, 1, false>(f32, layer, quant)                                            \
-                        : (s).j8 == 2 ? of<32, 2, false>(f32, layer, quant)                                            \
-                                      : of<32, 3, false>(f32, layer, quant))                                           \
-     : (s).tpr == 64 ? ((s).j8 <= 2 ? of<64, 2, false>(f32, layer, quant) : of<64, 3, false>(f32, layer, quant))       \
-     : (s).tpr == 128 ? ((s).j8 <= 2 ? of<128, 2, false>(f32, layer, quant) : of<128, 3, false>(f32, layer, quant))    \
-                      : ((s).j8 <= 2 ? of<256, 2, false>(f32, layer, quant) : of<256, 3, false>(f32, layer, quant)))
+template <int THREADS, int TPR, int J8, bool WIDE>
+BwdKernel bwd_of(bool f32, bool layer) {
+    if (f32)
+        return layer ? norm_gate_bwd_kernel<THREADS, TPR, 2 * J8, 4, true, WIDE>
+                     : norm_gate_bwd_kernel<THREADS, TPR, 2 * J8, 4, false, WIDE>;
+    return layer ? norm_gate_bwd_kernel<THREADS, TPR, J8, 8, true, WIDE> : norm_gate_bwd_kernel<THREADS, TPR, J8, 8, false, WIDE>;
+}
+BwdKernel backward_kernel(const Split& s, bool f32, bool layer) {
+    if (s.ctas > 1) return bwd_of<256, 256, 3, true>(f32, layer);
+    switch (s.tpr) {
+        case 32: return s.j8 == 1 ? bwd_of<384, 32, 1, false>(f32, layer) : bwd_of<384, 32, 2, false>(f32, layer);
+        case 64: return bwd_of<384, 64, 2, false>(f32, layer);
+        case 96: return bwd_of<384, 96, 2, false>(f32, layer);
+        case 128: return bwd_of<384, 128, 2, false>(f32, layer);
+        case 192: return bwd_of<384, 192, 2, false>(f32, layer);
+    }
+    return s.j8 == 2 ? bwd_of<256, 256, 2, false>(f32, layer) : bwd_of<256, 256, 3, false>(f32, layer);
+}
 
 }  // namespace
 
 int launch_norm_gate(const NormArgs& a0, bool f32, cudaStream_t stream) {
     NormArgs a = a0;
-    const Split s = split_of(a.C);
-    const FwdKernel kernel = FP4ATTN_NORM_KERNEL(fwd_of, s, f32, a.layer, a.codes != nullptr);
+    const Split s = forward_split(a.C);
+    const FwdKernel kernel = forward_kernel(s, f32, a.layer, a.codes != nullptr);
     a.cols = s.cols;
     a.slot_bytes = (uint32_t)s.cols * ((f32 ? 4 : 2) + (a.h ? 2 : 0));
     Shape sh;
-    const int st = shape_of(reinterpret_cast<const void*>(kernel), s, s.ctas > 1 ? 1 : FWD_THREADS / s.tpr, (size_t)12 * s.cols,
-                            a.slot_bytes, a.rows, sh);
+    const int st = shape_of(reinterpret_cast<const void*>(kernel), s, (size_t)12 * s.cols, a.slot_bytes, a.rows, sh);
     if (st != FP4ATTN_OK) return st;
     a.slots = sh.slots;
-    return launch(kernel, a, s.ctas > 1 ? s.tpr : FWD_THREADS, s, sh, stream);
+    return launch(kernel, a, s, sh, stream);
 }
 
-// Parts of a sample's rows: the longest work of a team, ceil(groups * parts /
-// teams) items of ceil(rows / parts) rows, is what the launch takes.
+// Parts of a sample's rows: the longest way of a team, ceil(groups * parts /
+// clusters) items of its share of ceil(rows / parts) rows each, is what the
+// launch takes.
 int64_t norm_backward_parts(int64_t rows, int64_t C, int64_t groups) {
     if (rows == 0 || groups == 0) return 1;
-    const Split s = split_of(C);
-    const int64_t rpg = rows / groups, teams = 148 / s.ctas * (NTHREADS / s.tpr);
-    int64_t most = (4 * teams + groups - 1) / groups;
+    const Split s = backward_split(C);
+    const int64_t rpg = rows / groups, clusters = 148 / s.ctas;
+    int64_t most = (4 * clusters + groups - 1) / groups;
     if (most > rpg) most = rpg;
+    if (s.ctas > 1) return most;  // how many clusters run at once is not known here: short items even that out
     int64_t best = 1, cost = -1;
     for (int64_t p = 1; p <= most; ++p) {
-        const int64_t c = ((groups * p + teams - 1) / teams) * ((rpg + p - 1) / p);
+        const int64_t part = (rpg + p - 1) / p;
+        const int64_t c = ((groups * p + clusters - 1) / clusters) * ((part + s.teams - 1) / s.teams);
         if (cost < 0 || c < cost) {
             cost = c;
             best = p;
@@ -958,15 +1104,16 @@ int64_t norm_backward_parts(int64_t rows, int64_t C, int64_t groups) {
 
 int launch_norm_gate_backward(const NormBwdArgs& a0, bool f32, cudaStream_t stream) {
     NormBwdArgs a = a0;
-    const Split s = split_of(a.C);
-    const BwdKernel kernel = FP4ATTN_NORM_KERNEL(bwd_of, s, f32, a.layer, false);
+    const Split s = backward_split(a.C);
+    const BwdKernel kernel = backward_kernel(s, f32, a.layer);
     a.cols = s.cols;
     a.slot_bytes = (uint32_t)s.cols * ((f32 ? 4 : 2) * (a.dy ? 2 : 1) + (a.h ? 4 : 2));
     Shape sh;
-    const int st = shape_of(reinterpret_cast<const void*>(kernel), s, NTHREADS / s.tpr, 0, a.slot_bytes, a.groups * a.parts, sh);
+    const int st = shape_of(reinterpret_cast<const void*>(kernel), s, (size_t)(s.teams > 1 ? 20 : 8) * s.cols, a.slot_bytes,
+                            a.groups * a.parts, sh);
     if (st != FP4ATTN_OK) return st;
     a.slots = sh.slots;
-    if (launch(kernel, a, NTHREADS, s, sh, stream) != FP4ATTN_OK) return FP4ATTN_ERR_CUDA;
+    if (launch(kernel, a, s, sh, stream) != FP4ATTN_OK) return FP4ATTN_ERR_CUDA;
     const int64_t blocks = (a.C + 31) / 32;
     if (launch_behind(norm_join_kernel, dim3((unsigned)(blocks * a.groups)), 256, 0, stream, 1, a) != cudaSuccess)
         return FP4ATTN_ERR_CUDA;
