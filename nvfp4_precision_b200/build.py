@@ -1,4 +1,5 @@
-"""Build the CUDA library ``libfp4attn.so`` in-tree for sm_100a.
+"""Build the CUDA library ``libfp4attn.so`` in-tree for sm_100a, and the
+extension through which Python makes its shortest calls.
 
     python -m nvfp4_precision_b200.build [--force] [--verbose]
 
@@ -11,6 +12,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,6 +24,10 @@ LIB = os.path.join(PKG, "libfp4attn.so")
 # check records FP4ATTN_ERR_RANGE instead of touching memory.  A debugging
 # build; the binding loads it when FP4ATTN_BOUNDS_CHECK=1.
 LIB_CHECKED = os.path.join(PKG, "libfp4attn_checked.so")
+
+# The calls of the linear layers and norms from Python (csrc/calls.cpp).
+CALLS = os.path.join(PKG, "_calls.so")
+CALLS_SRC = os.path.join(CSRC, "calls.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -35,7 +41,26 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def build_calls(force: bool = False) -> str:
+    deps = [CALLS_SRC, os.path.join(INCLUDE, "fp4attn.h")]
+    if not force and os.path.exists(CALLS) and all(os.path.getmtime(CALLS) >= os.path.getmtime(d) for d in deps):
+        return CALLS
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    tmp = CALLS + f".tmp{os.getpid()}"
+    includes = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{i}" for i in includes),
+                    CALLS_SRC, f"-L{root}/lib", f"-Wl,-rpath,{root}/lib", "-ltorch_python", "-ltorch", "-ltorch_cpu",
+                    "-lc10", "-lc10_cuda", "-o", tmp], check=True)
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
+    build_calls(force and not checked)
     out = LIB_CHECKED if checked else LIB
     deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) \
         + glob.glob(os.path.join(INCLUDE, "*.h"))

@@ -1087,11 +1087,16 @@ int64_t norm_backward_parts(int64_t rows, int64_t C, int64_t groups) {
     if (rows == 0 || groups == 0) return 1;
     const Split s = backward_split(C);
     const int64_t rpg = rows / groups, clusters = 148 / s.ctas;
-    int64_t most = (4 * clusters + groups - 1) / groups;
-    if (most > rpg) most = rpg;
-    if (s.ctas > 1) return most;  // how many clusters run at once is not known here: short items even that out
+    if (s.ctas > 1) {
+        // how many clusters run at once is not known here: short items even that out
+        const int64_t many = (4 * clusters + groups - 1) / groups;
+        return many < rpg ? many : rpg;
+    }
+    // the most parts for each number of rounds: more of them are shorter
     int64_t best = 1, cost = -1;
-    for (int64_t p = 1; p <= most; ++p) {
+    for (int64_t rounds = 1; rounds <= 4; ++rounds) {
+        int64_t p = rounds * clusters / groups;
+        p = p < 1 ? 1 : p > rpg ? rpg : p;
         const int64_t part = (rpg + p - 1) / p;
         const int64_t c = ((groups * p + clusters - 1) / clusters) * ((part + s.teams - 1) / s.teams);
         if (cost < 0 || c < cost) {

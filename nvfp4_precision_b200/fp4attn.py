@@ -8,7 +8,6 @@ no fallback implementation.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from typing import Optional
 
@@ -414,89 +413,30 @@ def fp4_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, softmax_sca
 
 # ------------------------------------------------- linear layers in NVFP4 --
 
-# The calls below cost a few microseconds of host time each, next to kernels
-# that take as long for one row: they look up the device and the stream once
-# and pass addresses as plain integers.
+# The calls below take a few microseconds on the device for one row.  Their
+# checks, outputs and library calls are made in native code (csrc/calls.cpp).
 
-def _current_device() -> int:
-    return torch.cuda.current_device()
-
-
-def _wrong_device(t: torch.Tensor):
-    """The library launches on the current device: a tensor of another one
-    would be reached by address only, so it is refused."""
-    raise ValueError(f"tensor on {t.device}: the library runs on the current CUDA device")
-
-
-def _raw_stream(dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev)
+def _load_calls():
+    path = os.path.join(_PKG, "_calls.so")
+    if not os.path.exists(path):
+        raise ImportError(f"extension {path} is missing; build it with `python -m nvfp4_precision_b200.build`")
+    from . import _calls
+    _calls.bind(Fp4AttnError, *(ctypes.cast(getattr(lib, "fp4attn_" + n), ctypes.c_void_p).value
+                                for n in ("quantize_rows", "dequant_rows", "gemm", "linear", "linear_backward", "norm_gate",
+                                          "norm_gate_backward")))
+    return _calls
 
 
-def _on_stream(fn):
-    """Runs a call given ``stream`` with that stream as the current one, so
-    that what it allocates (outputs, a workspace) is ordered there too."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kwargs):
-        if stream is None:
-            return fn(*args, **kwargs)
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream))
-        with torch.cuda.stream(stream):
-            return fn(*args, **kwargs)
-    return call
+_calls = _load_calls()
 
 
-def _rows_of(t: torch.Tensor, dev: int, what: str, dtype: torch.dtype, rows: int, cols: int):
-    """(address, row stride) of a [rows, cols] matrix of contiguous rows."""
-    assert t.shape == (rows, cols) and t.dtype is dtype, f"{what} is {dtype} [{rows}, {cols}]"
-    if t.get_device() != dev:
-        _wrong_device(t)
-    assert cols <= 1 or t.stride(1) == 1, f"{what}: rows must be contiguous"
-    return t.data_ptr(), t.stride(0)
-
-
-def _type_of(dtype: torch.dtype) -> int:
-    assert dtype is torch.bfloat16 or dtype is torch.float32, "rows are bf16 or fp32"
-    return F32 if dtype is torch.float32 else BF16
-
-
-def _packed_of(codes: torch.Tensor, scales: torch.Tensor, dev: int, what: str):
-    """(rows, K, address of the codes, address of the scales) of packed NVFP4 rows."""
-    assert codes.dtype is torch.uint8 and codes.dim() == 2 and codes.is_contiguous(), \
-        f"{what}: codes are uint8 [rows, K/2]"
-    rows, half = codes.shape
-    assert scales.dtype is torch.uint8 and scales.is_contiguous() \
-        and scales.numel() == (rows + 127) // 128 * ((half + 31) // 32) * 512, f"{what}: scale tiles of [{rows}, {2 * half}]"
-    if codes.get_device() != dev:
-        _wrong_device(codes)
-    if scales.get_device() != dev:
-        _wrong_device(scales)
-    return rows, 2 * half, codes.data_ptr(), scales.data_ptr()
-
-
-def _gscale_of(g: Optional[torch.Tensor], dev: int):
-    if g is None:
-        return None
-    assert g.dtype is torch.float32 and g.numel() == 1, "a scale is one fp32 on the device"
-    if g.get_device() != dev:
-        _wrong_device(g)
-    return g.data_ptr()
-
-
-def _vector_of(t: Optional[torch.Tensor], n: int, dev: int, what: str):
-    if t is None:
-        return None
-    assert t.shape == (n,) and t.dtype is torch.bfloat16 and (n <= 1 or t.stride(0) == 1), f"{what} is bf16 [{n}]"
-    if t.get_device() != dev:
-        _wrong_device(t)
-    return t.data_ptr()
-
-
-def _workspace_of(ws: torch.Tensor, dev: int):
-    assert ws.dtype is torch.uint8 and ws.is_contiguous(), "a workspace is contiguous uint8"
-    if ws.get_device() != dev:
-        _wrong_device(ws)
-    return ws.data_ptr(), ws.numel()
+def _on_stream(stream, fn, *args, **kwargs):
+    """fn(*args, **kwargs) with the given stream as the current one, so that
+    what it allocates (outputs, a workspace) is ordered there too."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return fn(*args, **kwargs)
 
 
 def fp4attn_scale_tile_bytes(rows: int, K: int) -> int:
@@ -545,154 +485,81 @@ def untile_scales(scales: torch.Tensor, rows: int, K: int) -> torch.Tensor:
     return t[:rows, :K // 16].contiguous()
 
 
-@_on_stream
 def fp4attn_quantize_rows(x: torch.Tensor, gscale: Optional[torch.Tensor] = None, dynamic_gscale: bool = False,
                           codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
-                          workspace: Optional[torch.Tensor] = None) -> dict:
+                          workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
     """NVFP4 rows of a bf16 or fp32 [rows, K] matrix (contiguous rows of any
     stride that is a multiple of 8, or 4 for fp32).  dynamic_gscale=True
     computes the per-tensor scale into gscale (allocated when None) instead of
     reading it.  Returns dict(codes, scales, gscale, workspace)."""
-    dev = _current_device()
-    rows, K = x.shape
-    xt = _type_of(x.dtype)
-    xp, ld = _rows_of(x, dev, "x", x.dtype, rows, K)
-    if codes is None:
-        codes = x.new_empty((rows, K // 2), dtype=torch.uint8)
-    if scales is None:
-        scales = x.new_empty(fp4attn_scale_tile_bytes(rows, K // 32 * 32), dtype=torch.uint8)
-    if K % 32 == 0:
-        r, k, cp, sp = _packed_of(codes, scales, dev, "output")
-        assert r == rows and k == K, f"output: packed rows of [{rows}, {K}]"
-    else:
-        cp, sp = codes.data_ptr(), scales.data_ptr()  # refused below
+    if stream is not None:
+        return _on_stream(stream, fp4attn_quantize_rows, x, gscale, dynamic_gscale, codes, scales, workspace)
     if workspace is None:
         workspace = new_linear_workspace(0, 0, 32, x.device)
-    ws, wsb = _workspace_of(workspace, dev)
-    if dynamic_gscale and gscale is None:
-        gscale = x.new_empty(1, dtype=torch.float32)
-    rc = lib.fp4attn_quantize_rows(xp, xt, ld, rows, K, _gscale_of(gscale, dev), DYNAMIC_GSCALE if dynamic_gscale else 0,
-                                   cp, sp, ws, wsb, _raw_stream(dev))
-    _check(rc, "fp4attn_quantize_rows")
+    codes, scales, gscale = _calls.quantize_rows(x, gscale, dynamic_gscale, codes, scales, workspace)
     return dict(codes=codes, scales=scales, gscale=gscale, workspace=workspace)
 
 
-@_on_stream
 def fp4attn_dequant_rows(codes: torch.Tensor, scales: torch.Tensor, gscale: Optional[torch.Tensor] = None,
-                         dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+                         dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """The values of packed NVFP4 rows, bf16 or fp32 [rows, K]."""
-    dev = _current_device()
-    rows, K, cp, sp = _packed_of(codes, scales, dev, "rows")
-    out = codes.new_empty((rows, K), dtype=dtype)
-    rc = lib.fp4attn_dequant_rows(cp, sp, _gscale_of(gscale, dev), rows, K, out.data_ptr(), _type_of(dtype),
-                                  _raw_stream(dev))
-    _check(rc, "fp4attn_dequant_rows")
-    return out
+    if stream is not None:
+        return _on_stream(stream, fp4attn_dequant_rows, codes, scales, gscale, dtype)
+    assert dtype is torch.bfloat16 or dtype is torch.float32, "rows are bf16 or fp32"
+    return _calls.dequant_rows(codes, scales, gscale, dtype is torch.float32)
 
 
-@_on_stream
 def fp4attn_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
                  x_gscale: Optional[torch.Tensor] = None, w_gscale: Optional[torch.Tensor] = None,
                  bias: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
-                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+                 workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y = g_x g_w x w^T + bias of packed NVFP4 x [M, K] and w [N, K]: bf16
     [M, N] (y may have any row stride)."""
-    dev = _current_device()
-    M, K, xc, xs = _packed_of(x_codes, x_scales, dev, "x")
-    N, K2, wc, wsc = _packed_of(w_codes, w_scales, dev, "w")
-    assert K == K2, "x and w share K"
-    if y is None:
-        y = x_codes.new_empty((M, N), dtype=torch.bfloat16)
-    yp, ld = _rows_of(y, dev, "y", torch.bfloat16, M, N)
+    if stream is not None:
+        return _on_stream(stream, fp4attn_gemm, x_codes, x_scales, w_codes, w_scales, x_gscale, w_gscale, bias, y, workspace)
     if workspace is None:
         workspace = new_linear_workspace(0, 0, 32, x_codes.device)
-    ws, wsb = _workspace_of(workspace, dev)
-    rc = lib.fp4attn_gemm(xc, xs, _gscale_of(x_gscale, dev), wc, wsc, _gscale_of(w_gscale, dev),
-                          _vector_of(bias, N, dev, "bias"), M, N, K, yp, ld, ws, wsb, _raw_stream(dev))
-    _check(rc, "fp4attn_gemm")
-    return y
+    return _calls.gemm(x_codes, x_scales, w_codes, w_scales, x_gscale, w_gscale, bias, y, workspace)
 
 
-@_on_stream
 def fp4attn_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
                    w_gscale: Optional[torch.Tensor] = None, x_gscale: Optional[torch.Tensor] = None,
                    dynamic_gscale: bool = False, bias: Optional[torch.Tensor] = None,
-                   y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+                   y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The NVFP4 linear layer of bf16 x [M, K]: quantises x (per-tensor scale
     x_gscale, None for 1, or computed with dynamic_gscale) and multiplies by
     the packed weight [N, K].  bf16 [M, N]."""
-    dev = _current_device()
-    N, K, wc, wsc = _packed_of(w_codes, w_scales, dev, "w")
-    M = x.shape[0]
-    xp, ldx = _rows_of(x, dev, "x", torch.bfloat16, M, K)
-    if y is None:
-        y = x.new_empty((M, N))
-    yp, ld = _rows_of(y, dev, "y", torch.bfloat16, M, N)
+    if stream is not None:
+        return _on_stream(stream, fp4attn_linear, x, w_codes, w_scales, w_gscale, x_gscale, dynamic_gscale, bias, y, workspace)
     if workspace is None:
-        workspace = new_linear_workspace(M, N, K, x.device)
-    ws, wsb = _workspace_of(workspace, dev)
-    rc = lib.fp4attn_linear(xp, ldx, _gscale_of(x_gscale, dev), DYNAMIC_GSCALE if dynamic_gscale else 0, wc, wsc,
-                            _gscale_of(w_gscale, dev), _vector_of(bias, N, dev, "bias"), M, N, K, yp, ld, ws, wsb,
-                            _raw_stream(dev))
-    _check(rc, "fp4attn_linear")
-    return y
+        workspace = new_linear_workspace(x.shape[0], w_codes.shape[0], x.shape[1], x.device)
+    return _calls.linear(x, w_codes, w_scales, w_gscale, x_gscale, dynamic_gscale, bias, y, workspace)
 
 
-@_on_stream
 def fp4attn_linear_backward(dy: torch.Tensor, x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.Tensor,
                             w_scales: torch.Tensor, x_gscale: Optional[torch.Tensor] = None,
                             w_gscale: Optional[torch.Tensor] = None, want_dx: bool = True, want_dw: bool = True,
-                            want_dbias: bool = True, workspace: Optional[torch.Tensor] = None):
+                            want_dbias: bool = True, workspace: Optional[torch.Tensor] = None, stream=None):
     """Straight-through gradients of fp4attn_linear for bf16 dy [M, N] and the
     packed operands of the forward: (dx bf16 [M, K], dw bf16 [N, K], dbias
     fp32 [N]), None in the place of one not wanted."""
-    dev = _current_device()
-    M, K, xc, xs = _packed_of(x_codes, x_scales, dev, "x")
-    N, K2, wc, wsc = _packed_of(w_codes, w_scales, dev, "w")
-    assert K == K2, "x and w share K"
-    dyp, ld = _rows_of(dy, dev, "dy", torch.bfloat16, M, N)
-    dx = dy.new_empty((M, K)) if want_dx else None
-    dw = dy.new_empty((N, K)) if want_dw else None
-    dbias = dy.new_empty(N, dtype=torch.float32) if want_dbias else None
+    if stream is not None:
+        return _on_stream(stream, fp4attn_linear_backward, dy, x_codes, x_scales, w_codes, w_scales, x_gscale, w_gscale, want_dx, want_dw,
+                          want_dbias, workspace)
     if workspace is None:
-        workspace = new_linear_backward_workspace(M, N, K, dy.device)
-    ws, wsb = _workspace_of(workspace, dev)
-    rc = lib.fp4attn_linear_backward(dyp, ld, xc, xs, _gscale_of(x_gscale, dev), wc, wsc, _gscale_of(w_gscale, dev),
-                                     M, N, K, dx.data_ptr() if want_dx else None, K,
-                                     dw.data_ptr() if want_dw else None, dbias.data_ptr() if want_dbias else None,
-                                     ws, wsb, _raw_stream(dev))
-    _check(rc, "fp4attn_linear_backward")
-    return dx, dw, dbias
+        workspace = new_linear_backward_workspace(*dy.shape, 2 * x_codes.shape[1], dy.device)
+    return _calls.linear_backward(dy, x_codes, x_scales, w_codes, w_scales, x_gscale, w_gscale, want_dx, want_dw, want_dbias,
+                                  workspace)
 
 
 # -------------------------------------------- the norms around a branch --
 
-def _norm_vectors(C: int, dev: int, post_weight, gate, pre_weight, scale, shift, groups: Optional[int]):
-    """(the C struct, number of samples) of the per-channel vectors."""
-    v = [_vector_of(post_weight, C, dev, "post_weight"), _vector_of(pre_weight, C, dev, "pre_weight")]
-    for t in (gate, scale, shift):
-        if t is None:
-            v += (None, 0)
-            continue
-        shape = t.shape
-        G = shape[0] if len(shape) == 2 else 1
-        assert shape[-1] == C and len(shape) <= 2 and t.dtype is torch.bfloat16 and t.stride(-1) == 1, \
-            f"gate, scale and shift are bf16 [groups, {C}]"
-        assert groups is None or groups == G, "gate, scale and shift share the number of samples"
-        groups = G
-        if t.get_device() != dev:
-            _wrong_device(t)
-        v += (t.data_ptr(), t.stride(0) if len(shape) == 2 else C)
-    return NormVectors(*v), 1 if groups is None else groups
-
-
-@_on_stream
 def fp4attn_norm_gate(x: torch.Tensor, h: Optional[torch.Tensor] = None, post_weight: Optional[torch.Tensor] = None,
                       gate: Optional[torch.Tensor] = None, pre_weight: Optional[torch.Tensor] = None,
                       scale: Optional[torch.Tensor] = None, shift: Optional[torch.Tensor] = None, eps: float = 1e-6,
                       flags: int = 0, groups: Optional[int] = None, want_y: bool = True, want_z: bool = True,
                       quantize: bool = False, z_gscale: Optional[torch.Tensor] = None,
-                      y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> dict:
+                      y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
     """y = x + gate * (post_weight * norm(h)) and z = norm(y) * pre_weight *
     (1 + scale) + shift, on bf16 or fp32 rows x [rows, C] and bf16 h (None for
     y = x).  RMS norms, or layer norms with flags=LAYER_NORM.  gate, scale and
@@ -701,76 +568,39 @@ def fp4attn_norm_gate(x: torch.Tensor, h: Optional[torch.Tensor] = None, post_we
     (None for 1), ready for fp4attn_gemm.  y may be given (x itself for an
     update in place).  Returns dict(y, z) or dict(y, z_codes, z_scales,
     workspace)."""
-    dev = _current_device()
-    rows, C = x.shape
-    dtype = x.dtype
-    xt = _type_of(dtype)
-    xp, ldx = _rows_of(x, dev, "x", dtype, rows, C)
-    hp, ldh = (None, 0) if h is None else _rows_of(h, dev, "h", torch.bfloat16, rows, C)
-    vec, G = _norm_vectors(C, dev, post_weight, gate, pre_weight, scale, shift, groups)
-    if y is None and want_y:
-        y = x.new_empty((rows, C))
-    yp, ldy = (None, 0) if y is None else _rows_of(y, dev, "y", dtype, rows, C)
-    z = codes = scales = None
-    zp = cp = sp = gz = ws = None
-    wsb = 0
-    if quantize:
-        codes = x.new_empty((rows, C // 2), dtype=torch.uint8)
-        scales = x.new_empty(fp4attn_scale_tile_bytes(rows, C // 32 * 32), dtype=torch.uint8)
-        cp, sp, gz = codes.data_ptr(), scales.data_ptr(), _gscale_of(z_gscale, dev)
-        if workspace is None:
-            workspace = new_linear_workspace(0, 0, 32, x.device)
-    elif want_z:
-        z = x.new_empty((rows, C), dtype=torch.bfloat16)
-        zp = z.data_ptr()
-    if workspace is not None:
-        ws, wsb = _workspace_of(workspace, dev)
-    rc = lib.fp4attn_norm_gate(xp, xt, ldx, hp, ldh, vec, rows, C, G, eps, flags, yp, ldy, zp, C, cp, sp, gz, ws, wsb,
-                               _raw_stream(dev))
-    _check(rc, "fp4attn_norm_gate")
-    if quantize:
-        return dict(y=y, z_codes=codes, z_scales=scales, workspace=workspace)
-    return dict(y=y, z=z)
+    if stream is not None:
+        return _on_stream(stream, fp4attn_norm_gate, x, h, post_weight, gate, pre_weight, scale, shift, eps, flags, groups, want_y,
+                          want_z, quantize, z_gscale, y, workspace)
+    if not quantize:
+        y, z = _calls.norm_gate(x, h, post_weight, gate, pre_weight, scale, shift, eps, flags, groups, want_y, want_z, False,
+                                None, y, workspace)
+        return {"y": y, "z": z}
+    if workspace is None:
+        workspace = new_linear_workspace(0, 0, 32, x.device)
+    y, codes, scales = _calls.norm_gate(x, h, post_weight, gate, pre_weight, scale, shift, eps, flags, groups, want_y, False,
+                                        True, z_gscale, y, workspace)
+    return dict(y=y, z_codes=codes, z_scales=scales, workspace=workspace)
 
 
-@_on_stream
 def fp4attn_norm_gate_backward(dz: torch.Tensor, dy: Optional[torch.Tensor], y: torch.Tensor,
                                h: Optional[torch.Tensor] = None, post_weight: Optional[torch.Tensor] = None,
                                gate: Optional[torch.Tensor] = None, pre_weight: Optional[torch.Tensor] = None,
                                scale: Optional[torch.Tensor] = None, eps: float = 1e-6, flags: int = 0,
-                               groups: Optional[int] = None, workspace: Optional[torch.Tensor] = None) -> dict:
+                               groups: Optional[int] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
     """Gradients of fp4attn_norm_gate for bf16 dz and dy (y's type, None for 0)
     from the forward's y and h: dict(dx, dh, dshift, dscale, dgate,
     dpre_weight, dpost_weight); dh, dgate and dpost_weight are None without h.
     Those of the vectors are fp32."""
-    dev = _current_device()
-    rows, C = y.shape
-    dtype = y.dtype
-    yt = _type_of(dtype)
-    yp, ldy = _rows_of(y, dev, "y", dtype, rows, C)
-    dzp, lddz = _rows_of(dz, dev, "dz", torch.bfloat16, rows, C)
-    dyp, lddy = (None, 0) if dy is None else _rows_of(dy, dev, "dy", dtype, rows, C)
-    hp, ldh = (None, 0) if h is None else _rows_of(h, dev, "h", torch.bfloat16, rows, C)
-    vec, G = _norm_vectors(C, dev, post_weight, gate, pre_weight, scale, None, groups)
+    if stream is not None:
+        return _on_stream(stream, fp4attn_norm_gate_backward, dz, dy, y, h, post_weight, gate, pre_weight, scale, eps, flags, groups,
+                          workspace)
     if workspace is None:
-        workspace = new_norm_backward_workspace(rows, C, G, y.device)
-    ws, wsb = _workspace_of(workspace, dev)
-    dx = y.new_empty((rows, C))
-    dh = dgate = dpost = dhp = None
-    if h is None:
-        dshift, dscale = y.new_empty((2, G, C), dtype=torch.float32).unbind(0)
-        dpre = y.new_empty(C, dtype=torch.float32)
-    else:
-        dh = y.new_empty((rows, C), dtype=torch.bfloat16)
-        dhp = dh.data_ptr()
-        dshift, dscale, dgate = y.new_empty((3, G, C), dtype=torch.float32).unbind(0)
-        dpre, dpost = y.new_empty((2, C), dtype=torch.float32).unbind(0)
-    rc = lib.fp4attn_norm_gate_backward(dzp, lddz, dyp, lddy, yp, ldy, yt, hp, ldh, vec, rows, C, G, eps, flags,
-                                        dx.data_ptr(), C, dhp, C, dshift.data_ptr(), dscale.data_ptr(),
-                                        None if h is None else dgate.data_ptr(), dpre.data_ptr(),
-                                        None if h is None else dpost.data_ptr(), ws, wsb, _raw_stream(dev))
-    _check(rc, "fp4attn_norm_gate_backward")
-    return dict(dx=dx, dh=dh, dshift=dshift, dscale=dscale, dgate=dgate, dpre_weight=dpre, dpost_weight=dpost)
+        samples = next((t.shape[0] for t in (gate, scale) if t is not None and t.dim() == 2), 1)
+        workspace = new_norm_backward_workspace(*y.shape, samples if groups is None else groups, device=y.device)
+    dx, dh, dshift, dscale, dgate, dpre, dpost = _calls.norm_gate_backward(dz, dy, y, h, post_weight, gate, pre_weight, scale,
+                                                                           eps, flags, groups, workspace)
+    return {"dx": dx, "dh": dh, "dshift": dshift, "dscale": dscale, "dgate": dgate, "dpre_weight": dpre,
+            "dpost_weight": dpost}
 
 
 # ------------------------------------------------------ differentiable --

@@ -266,3 +266,41 @@ def test_weights_quantised_right_before_they_are_used():
         for (a, b), (p, q) in zip(got, want):
             assert torch.equal(a, p) and torch.equal(b, q)
     assert fa.fp4attn_read_status(ws) == 0
+
+
+def test_wrong_kinds_are_refused():
+    """Types, shapes and layouts that the calls cannot take, and tensors off the device among those on it."""
+    fa = _fa()
+    gen = _gen(16)
+    x = _randn(gen, 4, 64)
+    w = fa.fp4attn_quantize_rows(_randn(gen, 8, 64))
+    c, s = w["codes"], w["scales"]
+    g = torch.ones(1, device="cuda")
+    nb = dict(dz=x, dy=x, y=x, h=x)
+    bad = [lambda: fa.fp4attn_quantize_rows(x.half()), lambda: fa.fp4attn_quantize_rows(x.t()),
+           lambda: fa.fp4attn_quantize_rows(x, gscale=g.double()), lambda: fa.fp4attn_quantize_rows(x, codes=c),
+           lambda: fa.fp4attn_quantize_rows(x, workspace=g), lambda: fa.fp4attn_dequant_rows(c, s[:-1]),
+           lambda: fa.fp4attn_dequant_rows(c.int(), s), lambda: fa.fp4attn_gemm(c, s, c[:, :16].contiguous(), s),
+           lambda: fa.fp4attn_gemm(c, s, c, s, bias=g), lambda: fa.fp4attn_gemm(c, s, c, s, y=x),
+           lambda: fa.fp4attn_linear(x.float(), c, s), lambda: fa.fp4attn_linear(x[:, :32], c, s),
+           lambda: fa.fp4attn_linear_backward(x, c, s, c, s), lambda: fa.fp4attn_norm_gate(x, x.float()),
+           lambda: fa.fp4attn_norm_gate(x, x[:2]), lambda: fa.fp4attn_norm_gate(x, x, post_weight=x),
+           lambda: fa.fp4attn_norm_gate(x, x, gate=x[:2], scale=x[:1]), lambda: fa.fp4attn_norm_gate(x, x, gate=x[:2], groups=4),
+           lambda: fa.fp4attn_norm_gate(x, x, pre_weight=x[0].float()), lambda: fa.fp4attn_norm_gate(x, y=x.float()),
+           lambda: fa.fp4attn_norm_gate_backward(**{**nb, "dz": x.float()}),
+           lambda: fa.fp4attn_norm_gate_backward(**{**nb, "dy": x.float()}),
+           lambda: fa.fp4attn_norm_gate_backward(**{**nb, "h": x[:3]})]
+    for call in bad:
+        with pytest.raises(AssertionError):
+            call()
+    for call in (lambda: fa.fp4attn_linear(x, c, s.cpu()), lambda: fa.fp4attn_linear(x, c, s, g.cpu()),
+                 lambda: fa.fp4attn_norm_gate(x, x.cpu()), lambda: fa.fp4attn_norm_gate(x, x, gate=x[:1].cpu()),
+                 lambda: fa.fp4attn_gemm(c, s, c, s, workspace=torch.zeros(4096, dtype=torch.uint8))):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call()
+    for call in (lambda: fa.fp4attn_quantize_rows(_randn(gen, 4, 72)[:, :40]), lambda: fa.fp4attn_norm_gate(_randn(gen, 4, 60)),
+                 lambda: fa.fp4attn_norm_gate(_randn(gen, 4, 72), quantize=True),
+                 lambda: fa.fp4attn_norm_gate(x, gate=x[:3]), lambda: fa.fp4attn_norm_gate(x, eps=-1.0),
+                 lambda: fa.fp4attn_linear(x, c, s, workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(fa.Fp4AttnError):
+            call()
