@@ -420,7 +420,6 @@ struct PairCfg {
     static constexpr uint32_t STAGE = 2 * P_BYTES + SFP_BYTES + SFQ_BYTES;
     static constexpr int STAGES = 5;
     static constexpr uint32_t ACC1 = 192;  // the second accumulator shares 64 columns with the first
-    static constexpr int OVERLAP = 64;
     static_assert(STAGE % 1024 == 0, "stages keep the swizzle's alignment");
     static_assert(SF_COL + CHUNKS * 12 <= TMEM_COLS, "TMEM: scale factors");
 };

@@ -304,3 +304,87 @@ def test_wrong_kinds_are_refused():
                  lambda: fa.fp4attn_linear(x, c, s, workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))):
         with pytest.raises(fa.Fp4AttnError):
             call()
+
+
+def test_results_in_place_and_strided_through_the_c_abi():
+    """What the header allows and the binding never asks for: gradients over their inputs, rows of other strides."""
+    fa = _fa()
+    gen = _gen(18)
+    M, C, G = 50, 1160, 2
+    for dtype in (BF, torch.float32):
+        y, dy = _randn(gen, M, C, dtype=dtype), _randn(gen, M, C, dtype=dtype)
+        h, dz = _randn(gen, M, C), _randn(gen, M, C)
+        gate = _randn(gen, G, C)
+        ws = fa.new_norm_backward_workspace(M, C, G)
+        want = fa.fp4attn_norm_gate_backward(dz, dy, y, h, gate=gate, workspace=ws)
+        vec = fa.NormVectors(gate=gate.data_ptr(), gate_stride=C)
+        t = fa.F32 if dtype == torch.float32 else fa.BF16
+        for over in ("dz", "h"):
+            dx, dzc, hc = dy.clone(), dz.clone(), h.clone()
+            dh = dzc if over == "dz" else hc
+            rc = fa.lib.fp4attn_norm_gate_backward(dzc.data_ptr(), C, dx.data_ptr(), C, y.data_ptr(), C, t, hc.data_ptr(), C,
+                                                   vec, M, C, G, 1e-6, 0, dx.data_ptr(), C, dh.data_ptr(), C, None, None, None,
+                                                   None, None, ws.data_ptr(), ws.numel(), fa._stream(None))
+            assert rc == 0 and torch.equal(dx, want["dx"]) and torch.equal(dh, want["dh"])
+        # outputs between rows of other data
+        big = {k: torch.full((M, C + 16), 3.0, dtype=want[k].dtype, device="cuda") for k in ("dx", "dh")}
+        rc = fa.lib.fp4attn_norm_gate_backward(dz.data_ptr(), C, dy.data_ptr(), C, y.data_ptr(), C, t, h.data_ptr(), C, vec, M, C,
+                                               G, 1e-6, 0, big["dx"].data_ptr(), C + 16, big["dh"].data_ptr(), C + 16, None, None,
+                                               None, None, None, ws.data_ptr(), ws.numel(), fa._stream(None))
+        assert rc == 0
+        for k, b in big.items():
+            assert torch.equal(b[:, :C], want[k]) and (b[:, C:] == 3.0).all()
+        z = torch.full((M, C + 8), 3.0, dtype=BF, device="cuda")
+        rc = fa.lib.fp4attn_norm_gate(y.data_ptr(), t, C, h.data_ptr(), C, vec, M, C, G, 1e-6, 0, None, 0, z.data_ptr(), C + 8,
+                                      None, None, None, None, 0, fa._stream(None))
+        assert rc == 0 and (z[:, C:] == 3.0).all()
+        assert torch.equal(z[:, :C], fa.fp4attn_norm_gate(y, h, gate=gate)["z"])
+    # dx of the linear layer, whole tiles and split ones
+    for M, N, K in ((700, 264, 96), (5000, 4000, 544)):
+        x, w = fa.fp4attn_quantize_rows(_randn(gen, M, K)), fa.fp4attn_quantize_rows(_randn(gen, N, K))
+        dy = _randn(gen, M, N)
+        ws = fa.new_linear_backward_workspace(M, N, K)
+        want = fa.fp4attn_linear_backward(dy, x["codes"], x["scales"], w["codes"], w["scales"], want_dw=False, want_dbias=False)[0]
+        big = torch.full((M, K + 24), 3.0, dtype=BF, device="cuda")
+        rc = fa.lib.fp4attn_linear_backward(dy.data_ptr(), N, None, None, None, w["codes"].data_ptr(), w["scales"].data_ptr(), None,
+                                            M, N, K, big.data_ptr(), K + 24, None, None, ws.data_ptr(), ws.numel(),
+                                            fa._stream(None))
+        assert rc == 0 and torch.equal(big[:, :K], want) and (big[:, K:] == 3.0).all()
+        assert fa.fp4attn_read_status(ws) == 0
+
+
+def test_chains_through_launches_that_overlap():
+    """Each call reads what the one before has just written, on one stream with no wait between them."""
+    fa = _fa()
+    gen = _gen(19)
+    M, C = 640, 512
+    w = fa.fp4attn_quantize_rows(_randn(gen, C, C, std=C ** -0.5), dynamic_gscale=True)
+    x, h = _randn(gen, M, C), _randn(gen, M, C)
+    ws = fa.new_linear_workspace(M, C, C)
+    bws, nws = fa.new_linear_backward_workspace(M, C, C), fa.new_norm_backward_workspace(M, C, 1)
+
+    def chain(wait):
+        outs, t = [], h
+        for i in range(6):
+            n = fa.fp4attn_norm_gate(x, t, workspace=ws)
+            wait()
+            q = fa.fp4attn_quantize_rows(n["z"], dynamic_gscale=i % 2 == 0, workspace=ws)
+            wait()
+            t = fa.fp4attn_gemm(q["codes"], q["scales"], w["codes"], w["scales"], q["gscale"], w["gscale"], workspace=ws)
+            wait()
+            t = fa.fp4attn_linear(t, w["codes"], w["scales"], w["gscale"], dynamic_gscale=i % 2 == 1, workspace=ws)
+            wait()
+            g = fa.fp4attn_linear_backward(t, q["codes"], q["scales"], w["codes"], w["scales"], q["gscale"], w["gscale"],
+                                           workspace=bws)
+            wait()
+            b = fa.fp4attn_norm_gate_backward(g[0], None, n["y"], t, workspace=nws)
+            wait()
+            outs += [t, *g, *b.values()]
+        return outs
+
+    want = chain(torch.cuda.synchronize)
+    for _ in range(5):
+        got = chain(lambda: None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+    assert all(fa.fp4attn_read_status(v) == 0 for v in (ws, bws, nws))
