@@ -419,21 +419,29 @@ struct Plan {
 // pairs in order, so a pair has the longest way to go that starts first.  Either
 // all tiles of a small product are split, or the last ones, which do not fill a
 // round of the pairs any more.  A stage costs what its bytes take (48, 32 or 24
-// KB at about 42 bytes a clock), a unit its epilogue's part that nothing hides.
+// KB at about 42 bytes a clock).  An epilogue takes about 18 clocks a column and
+// hides under the next unit's products unless the tile takes all of TMEM (512
+// columns); of a split tile, in fp32, twice that.  The plans are within ten
+// percent of the best ones found at 3001 x 200 x 544, 1000 x 64 x 256, 4096 x 256
+// x 1024, 256 x 4096 x 4096 and 8192 x 1024 x 1024 (M x N x K).
 Plan make_plan(int64_t M, int64_t N, int64_t K, bool want_dw, bool want_dx) {
     Plan best{};
     double best_cost = -1.0;
     const int64_t rows[2] = {want_dw ? N : 0, want_dx ? M : 0}, contraction[2] = {M, N};
     for (int tn = 512; tn >= 128; tn /= 2) {
-        const double per_stage = tn == 512 ? 1170.0 : tn == 256 ? 780.0 : 585.0, per_unit = tn == 512 ? 4000.0 : 1500.0;
+        const double per_stage = tn == 512 ? 1170.0 : tn == 256 ? 780.0 : 585.0;
         const int64_t ct = (K + tn - 1) / tn;
         int64_t tiles[2], stages[2];
         for (int i = 0; i < 2; ++i) {
             tiles[i] = (rows[i] + BM - 1) / BM * ct;
             stages[i] = (contraction[i] + BKC - 1) / BKC;
         }
-        auto unit = [&](int i, int split) { return (double)((stages[i] + split - 1) / split) * per_stage + per_unit; };
-        auto join = [&](int64_t tail, int split) { return 4000.0 + (double)tail * split * BM * tn * 8.0 / 4000.0; };
+        auto unit = [&](int i, int split) {
+            const double products = (double)((stages[i] + split - 1) / split) * per_stage;
+            const double epilogue = 18.0 * tn * (split > 1 ? 2.0 : 1.0);
+            return tn == 512 ? products + epilogue : (products > epilogue ? products : epilogue) + 3000.0;
+        };
+        auto join = [&](int64_t tail, int split) { return 5000.0 + (double)tail * split * BM * tn * 4.0 / 2500.0; };
         auto offer = [&](double cost, const int64_t (&whole)[2], const int (&split)[2], int first) {
             if (best_cost >= 0.0 && cost >= best_cost) return;
             best_cost = cost;
