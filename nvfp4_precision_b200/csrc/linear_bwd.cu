@@ -439,9 +439,9 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, bool want_dw, bool want_dx) {
         auto unit = [&](int i, int split) {
             const double products = (double)((stages[i] + split - 1) / split) * per_stage;
             const double epilogue = 18.0 * tn * (split > 1 ? 2.0 : 1.0);
-            return tn == 512 ? products + epilogue : (products > epilogue ? products : epilogue) + 3000.0;
+            return tn == 512 ? products + epilogue : (products > epilogue ? products : epilogue) + 1500.0;
         };
-        auto join = [&](int64_t tail, int split) { return 5000.0 + (double)tail * split * BM * tn * 4.0 / 2500.0; };
+        auto join = [&](int64_t tail, int split) { return 5000.0 + (double)tail * split * (100.0 + BM * tn * 4.0 / 2500.0); };
         auto offer = [&](double cost, const int64_t (&whole)[2], const int (&split)[2], int first) {
             if (best_cost >= 0.0 && cost >= best_cost) return;
             best_cost = cost;
