@@ -255,16 +255,22 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) norm_gate_kernel(const __grid_
     const uint32_t ring_u = smem_u32(ring), bars_u = smem_u32(&bars[team.index * MAX_SLOTS]);
     const int64_t clusters = gridDim.x / team.ranks, cluster = blockIdx.x / team.ranks;
     const int64_t r0 = a.rows * cluster / clusters, r1 = a.rows * (cluster + 1) / clusters;
-    int64_t next = r0 + team.index;  // rows r0 + index, + TEAMS, ...
-    auto fill = [&](int slot) {      // of the next row, by thread 0
+    // thread 0's rows ahead: r0 + index, + TEAMS, ...
+    int ahead = (int)((r1 - r0 - team.index + TEAMS - 1) / TEAMS);
+    const uint8_t* x_next = static_cast<const uint8_t*>(a.x) + ((r0 + team.index) * a.ldx + c0) * ES;
+    const __nv_bfloat16* h_next = a.h + ((r0 + team.index) * a.ldh + c0);
+    const int64_t x_step = (int64_t)TEAMS * a.ldx * ES, h_step = (int64_t)TEAMS * a.ldh;
+    auto fill = [&](int slot) {
         const uint32_t bar = bars_u + 8u * slot, at = ring_u + a.slot_bytes * slot;
         mbar_arrive_expect_tx(bar, x_bytes + h_bytes);
-        bulk_load(at, static_cast<const uint8_t*>(a.x) + (next * a.ldx + c0) * ES, x_bytes, bar);
-        if (has_h) bulk_load(at + x_bytes, a.h + next * a.ldh + c0, h_bytes, bar);
-        next += TEAMS;
+        bulk_load(at, x_next, x_bytes, bar);
+        if (has_h) bulk_load(at + x_bytes, h_next, h_bytes, bar);
+        x_next += x_step;
+        h_next += h_step;
+        --ahead;
     };
     if (t == 0)
-        for (int s = 0; s < a.slots && next < r1; ++s) fill(s);
+        for (int s = 0; s < a.slots && ahead > 0; ++s) fill(s);
     const float inv_c = 1.0f / (float)a.C;
     const int sf_shift = 8 * ((t * U / 16) & 3);  // TPR U channels are whole chunks of 64
 
@@ -396,7 +402,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) norm_gate_kernel(const __grid_
                 team.sync();
             }
             // every thread has its row: the slot is free
-            if (t == 0 && next < r1 && !*abort_flag) fill(slot);
+            if (t == 0 && ahead > 0 && !*abort_flag) fill(slot);
             if (++slot == a.slots) {
                 slot = 0;
                 parity ^= 1;
@@ -576,25 +582,40 @@ __global__ void __launch_bounds__(THREADS, 1) norm_gate_bwd_kernel(const __grid_
         begin = g * a.rows_per_group + a.rows_per_group * p / a.parts;
         end = g * a.rows_per_group + a.rows_per_group * (p + 1) / a.parts;
     };
-    // the rows ahead of this team, over its CTA's items
-    int64_t ahead_item = first_item, ahead = 0, ahead_end = 0;
+    // thread 0's rows ahead, over the CTA's items: of an item, `left` and where the next one lies
+    int64_t ahead_item = first_item;
+    int left = 0;
+    const uint8_t *y_next = nullptr, *dy_next = nullptr;
+    const __nv_bfloat16 *dz_next = nullptr, *h_next = nullptr;
+    const int64_t y_step = (int64_t)TEAMS * a.ldy * ES, dy_step = (int64_t)TEAMS * a.lddy * ES,
+                  dz_step = (int64_t)TEAMS * a.lddz, h_step = (int64_t)TEAMS * a.ldh;
     auto seek = [&]() {  // from a new item on to one that has a row for this team
         for (; ahead_item < items; ahead_item += clusters) {
-            item_rows(ahead_item, ahead, ahead_end);
-            ahead += team.index;
-            if (ahead < ahead_end) return;
+            int64_t begin, end;
+            item_rows(ahead_item, begin, end);
+            begin += team.index;
+            if (begin >= end) continue;
+            left = (int)((end - begin + TEAMS - 1) / TEAMS);
+            y_next = static_cast<const uint8_t*>(a.y) + (begin * a.ldy + c0) * ES;
+            dy_next = static_cast<const uint8_t*>(a.dy) + (begin * a.lddy + c0) * ES;
+            dz_next = a.dz + (begin * a.lddz + c0);
+            h_next = a.h + (begin * a.ldh + c0);
+            return;
         }
     };
-    auto fill_next = [&](int slot) {  // by thread 0
-        if (ahead_item >= items) return;
+    auto fill_next = [&](int slot) {
+        if (left == 0) return;  // no item any more
         const uint32_t bar = bars_u + 8u * slot, at = ring_u + a.slot_bytes * slot;
         mbar_arrive_expect_tx(bar, row_bytes);
-        bulk_load(at, static_cast<const uint8_t*>(a.y) + (ahead * a.ldy + c0) * ES, res_bytes, bar);
-        if (has_dy) bulk_load(at + at_dy, static_cast<const uint8_t*>(a.dy) + (ahead * a.lddy + c0) * ES, res_bytes, bar);
-        bulk_load(at + at_dz, a.dz + ahead * a.lddz + c0, half_bytes, bar);
-        if (has_h) bulk_load(at + at_h, a.h + ahead * a.ldh + c0, half_bytes, bar);
-        ahead += TEAMS;
-        if (ahead >= ahead_end) {
+        bulk_load(at, y_next, res_bytes, bar);
+        if (has_dy) bulk_load(at + at_dy, dy_next, res_bytes, bar);
+        bulk_load(at + at_dz, dz_next, half_bytes, bar);
+        if (has_h) bulk_load(at + at_h, h_next, half_bytes, bar);
+        y_next += y_step;
+        dy_next += dy_step;
+        dz_next += dz_step;
+        h_next += h_step;
+        if (--left == 0) {
             ahead_item += clusters;
             seek();
         }
