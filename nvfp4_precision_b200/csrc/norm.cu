@@ -672,14 +672,20 @@ __global__ void __launch_bounds__(THREADS, 1) norm_gate_bwd_kernel(const __grid_
             }
         }
         auto gate_of = [&](int j, int u, float2(&v)[P]) {
-            if (!HELD) return vector(0, u, v);
+            if constexpr (HELD) {
 #pragma unroll
-            for (int i = 0; i < P; ++i) v[i] = held_A[j][i];
+                for (int i = 0; i < P; ++i) v[i] = held_A[j][i];
+            } else {
+                vector(0, u, v);
+            }
         };
         auto pre_of = [&](int j, int u, float2(&v)[P]) {
-            if (!HELD) return vector(1, u, v);
+            if constexpr (HELD) {
 #pragma unroll
-            for (int i = 0; i < P; ++i) v[i] = held_B[j][i];
+                for (int i = 0; i < P; ++i) v[i] = held_B[j][i];
+            } else {
+                vector(1, u, v);
+            }
         };
         for (int64_t row = begin + team.index; row < end; row += TEAMS) {
             const bool ok = mbar_wait(bars_u + 8u * slot, parity, abort_flag, a.status, kLimitNs);
