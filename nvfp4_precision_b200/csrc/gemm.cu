@@ -407,9 +407,14 @@ __global__ void __launch_bounds__(THREADS, 1)
 // Each CTA loads 128 rows of the lane side and 128 of the column side per stage
 // and both read each other's half of the latter through the pair: 8 KB of codes
 // in and 8 KB read per 128 clocks of tensor work, where a single CTA's 128 x 256
-// tile needs 12 and 12 and is held up by its shared memory.  The scales of the
-// column side are wanted whole by both.  The CTA of rank 0 issues the products;
-// accumulators and scale factors lie in TMEM as in the kernel above.
+// tile needs 12 and 12.  The scales of the column side are wanted whole by both.
+// The CTA of rank 0 issues the products; accumulators and scale factors lie in
+// TMEM as in the kernel above.
+//
+// 109568 x 6144 x 6144: 1.58 ms, 5.2 PFLOP/s (1.85 ms on single CTAs).  A stage's
+// products take 512 clocks and its 38 KB come from L2 in about 900 (42 bytes a
+// clock and SM, 12 TB/s in all): on operands at rest the same loop reaches 7.4
+// PFLOP/s at K = 24576.  Larger tiles do not fit TMEM beside the scale factors.
 
 constexpr int PAIR_TILE = 256;
 constexpr int PAIR_THREADS = 32 * (STORE_WARPS + 2);

@@ -4,20 +4,28 @@
 //   dw = g_x dy^T X~     [N, K]      the forward's operands, exact in bf16
 //   dbias = column sums of dy
 //
-// The operands are expanded to bf16 once (a few percent of the products' time)
-// and both products run in ONE persistent launch on the BF16 tensor cores:
+// The operands are expanded to bf16 once, in a launch that also takes the partial
+// column sums (50 us of 825 at 8192 x 6144 x 6144, mostly HBM), and both products
+// run in ONE persistent launch on the BF16 tensor cores:
 //   * a CTA pair owns a 256 x TN tile (tcgen05 cta_group::2): each CTA loads
 //     128 rows of one operand and half of the other's TN columns and keeps 128
-//     rows of the accumulator.  A single CTA would read 12 KB of operands and
-//     take in as many for 128 clocks of tensor work, more than its shared
-//     memory passes; the pair needs 8 KB;
+//     rows of the accumulators;
+//   * what bounds large products is how fast L2 feeds the SMs (about 42 bytes a
+//     clock each, 12 TB/s in all): a 256-column tile takes 64 bytes a clock of
+//     tensor work, a 512-column one 48.  At 8192 x 6144 x 6144 the launch takes
+//     753 us with 512 columns (1.64 PFLOP/s, the tensor pipe 92% busy; 820 us with
+//     256, of which 665 remain when the loads are left out), and longer when the
+//     power cap lowers the clock;
 //   * W~ and X~ are taken as they lie: their contraction runs down the rows, so
 //     they enter as MN-major tiles, and so does dy for dw.  Nothing is
 //     transposed in memory.  One box shape (64 x 64, 128B swizzle) serves all;
-//   * two accumulators fill TMEM, so the epilogue of a tile runs under the
-//     products of the next;
-//   * few tiles and a long contraction: a tile is split into parts, fp32 parts
-//     meet in the workspace and a last launch adds them in order.
+//   * accumulators of 256 columns: narrow tiles take turns between the two that
+//     TMEM holds, and the epilogue of one runs under the products of the next;
+//     a 512-column tile takes both, and its first half is stored while the
+//     second still waits for its last products;
+//   * tiles may be split along the contraction (all of a small product's, or the
+//     last ones, which do not fill a round of the pairs): fp32 parts meet in the
+//     workspace and a last launch adds them in order.
 // Every wait is bounded (FP4ATTN_ERR_TIMEOUT).
 #include <cuda_bf16.h>
 

@@ -25,8 +25,13 @@
 // The forward's z can leave as NVFP4 rows (rounded to bf16 first, as the
 // quantiser of a bf16 z would see it), so that the next linear layer reads
 // 9/16 byte a value instead of writing, reading and quantising 2-byte ones.
-// The teams' column sums meet in the workspace and are added in order: no
-// atomics, equal calls give equal bits.
+// The CTAs' column sums meet in the workspace and are added in order: no atomics,
+// equal calls give equal bits.
+//
+// Forward 109568 x 6144, fp32 residual: 1.37 ms, 5.9 TB/s; backward 36864 x 6144:
+// bf16 458 us (5.9 TB/s), layer norm 547, fp32 618 (6.6 TB/s).  What is left in
+// the bf16 layer norms, quantised ones above all (36864 x 6144: 377 us, 226 at
+// HBM's rate), is instructions: 57% of the issue slots, the rest latency.
 #include <type_traits>
 
 #include <cuda_bf16.h>
