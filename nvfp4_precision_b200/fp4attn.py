@@ -654,7 +654,7 @@ class FP4LinearSTE(torch.autograd.Function):
     def backward(ctx, dy):
         _refuse_capture("FP4LinearSTE")
         xc, xs, gx, wc, wsc, gw = ctx.saved_tensors
-        rows = _aligned_rows(dy.to(torch.bfloat16).reshape(-1, wc.shape[0]))
+        rows = _aligned_rows(dy.to(torch.bfloat16).reshape(xc.shape[0], wc.shape[0]))
         ws = new_linear_backward_workspace(xc.shape[0], wc.shape[0], 2 * wc.shape[1], dy.device)
         dx, dw, db = fp4attn_linear_backward(rows, xc, xs, wc, wsc, gx, gw, want_dx=ctx.needs_input_grad[0],
                                              want_dw=ctx.needs_input_grad[1], want_dbias=ctx.needs_input_grad[2],
