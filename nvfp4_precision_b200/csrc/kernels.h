@@ -226,7 +226,17 @@ struct GemmFp4Args {
 };
 int launch_gemm_fp4(const GemmFp4Args& a, cudaStream_t stream);
 
-// Its straight-through gradients (linear_bwd.cu).
+// Its straight-through gradients (linear_bwd.cu): how the two products (dw, then
+// dx) are cut up ...
+struct LinearBwdPlan {
+    int tn;  // columns of a tile
+    int64_t tiles[2], whole[2];
+    int split[2];  // of the tiles behind the whole ones
+    int first;     // the product whose units go first: the longer ones
+};
+LinearBwdPlan linear_backward_plan(int64_t M, int64_t N, int64_t K, bool want_dw, bool want_dx);
+size_t linear_backward_part_bytes(const LinearBwdPlan& plan);
+// ... and the call.
 struct LinearBwdArgs {
     const __nv_bfloat16* dy;
     int64_t ld_dy;
@@ -246,6 +256,7 @@ struct LinearBwdArgs {
     __nv_bfloat16* x_bf16;  // [M][K]
     float* colsum_part;     // COLSUM_PARTS * N
     float* part;            // linear_backward_part_bytes
+    LinearBwdPlan plan;     // for the gradients that are asked for
     int* status;
 };
 // Blocks of its first launch, by what they do.
@@ -255,7 +266,6 @@ struct BwdPrepare {
     int w_tiles;             // 128 x 128 tiles of w; the rest are x's
 };
 cudaError_t launch_backward_prepare(const LinearBwdArgs& a, int& colsum_parts, cudaStream_t stream);
-size_t linear_backward_part_bytes(int64_t M, int64_t N, int64_t K);
 int launch_linear_backward(const LinearBwdArgs& a, cudaStream_t stream);
 
 // ---- the norms around a branch (norm.cu) ----

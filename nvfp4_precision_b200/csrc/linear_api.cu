@@ -220,7 +220,13 @@ int fp4attn_linear(const void* x, int64_t x_stride, float* gx, uint32_t flags, c
 
 size_t fp4attn_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     if (check_mnk(M, N, K) != FP4ATTN_OK) return WS_STATUS_BYTES;
-    return lbws_part_offset(M, N, K) + round256(linear_backward_part_bytes(M, N, K));
+    // for any choice of gradients
+    size_t parts = 0;
+    for (int want = 1; want < 4; ++want) {
+        const size_t b = linear_backward_part_bytes(linear_backward_plan(M, N, K, want & 1, want & 2));
+        parts = b > parts ? b : parts;
+    }
+    return lbws_part_offset(M, N, K) + round256(parts);
 }
 
 int fp4attn_linear_backward(const void* dy, int64_t dy_stride, const uint8_t* x_codes, const uint8_t* x_scales,
@@ -229,7 +235,8 @@ int fp4attn_linear_backward(const void* dy, int64_t dy_stride, const uint8_t* x_
                             size_t workspace_bytes, cudaStream_t stream) {
     const int st = check_mnk(M, N, K);
     if (st != FP4ATTN_OK) return st;
-    if (!good(workspace) || workspace_bytes < fp4attn_linear_backward_workspace_bytes(M, N, K))
+    const LinearBwdPlan plan = linear_backward_plan(M, N, K, dw != nullptr, dx != nullptr);
+    if (!good(workspace) || workspace_bytes < lbws_part_offset(M, N, K) + round256(linear_backward_part_bytes(plan)))
         return FP4ATTN_ERR_WORKSPACE;
     if (!aligned4(gx) || !aligned4(gw) || !aligned4(dbias)) return FP4ATTN_ERR_INVALID_ARG;
     if (dx && M > 0 && bad_rows(dx, dx_stride, M, K, 8)) return FP4ATTN_ERR_INVALID_ARG;
@@ -268,6 +275,7 @@ int fp4attn_linear_backward(const void* dy, int64_t dy_stride, const uint8_t* x_
     a.x_bf16 = reinterpret_cast<__nv_bfloat16*>(ws + lbws_x_offset(N, K));
     a.colsum_part = reinterpret_cast<float*>(ws + lbws_colsum_offset(M, N, K));
     a.part = reinterpret_cast<float*>(ws + lbws_part_offset(M, N, K));
+    a.plan = plan;
     a.status = static_cast<int*>(workspace);
     return clear_error(launch_linear_backward(a, stream));
 }

@@ -415,94 +415,78 @@ bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int6
                              CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// How the two products (dw, then dx) are cut up.
-struct Plan {
-    int tn;
-    int64_t tiles[2], whole[2];
-    int split[2];
-    int first;  // the product whose units go first: the longer ones
-};
-
 // Tile width and splits by a model of the launch in clocks: units go round the
-// pairs in order, so a pair has the longest way to go that starts first.  Either
-// all tiles of a small product are split, or the last ones, which do not fill a
-// round of the pairs any more.  A stage costs what its bytes take (48, 32 or 24
-// KB at about 42 bytes a clock).  An epilogue takes about 18 clocks a column and
-// hides under the next unit's products unless the tile takes all of TMEM (512
-// columns); of a split tile, in fp32, twice that.  The plans are within ten
-// percent of the best ones found at 3001 x 200 x 544, 1000 x 64 x 256, 4096 x 256
-// x 1024, 256 x 4096 x 4096 and 8192 x 1024 x 1024 (M x N x K).
-Plan make_plan(int64_t M, int64_t N, int64_t K, bool want_dw, bool want_dx) {
-    Plan best{};
+// pairs in order, the longer ones first, so a pair has the longest way to go that
+// starts first.  Either product may be split (few tiles, a long contraction), and
+// the last tiles of the second, which do not fill a round of the pairs any more.
+// A stage costs what its bytes take (48, 32 or 24 KB at about 40 bytes a clock).
+// An epilogue takes about 18 clocks a column and hides under the next unit's
+// products unless the tile takes all of TMEM (512 columns: 30, with the pause of
+// the loads); of a split tile, in fp32, twice that.  The plans are within ten percent of the best ones found at
+// 3001 x 200 x 544, 1000 x 64 x 256, 4096 x 256 x 1024, 256 x 4096 x 4096 and 8192
+// x 1024 x 1024 (M x N x K); with splits of small totals only, 28972 x 976 x 928
+// took 231 us (now 131) and 100 x 15912 x 3328 142 (102).
+LinearBwdPlan make_plan(int64_t M, int64_t N, int64_t K, bool want_dw, bool want_dx) {
+    LinearBwdPlan best{};
     double best_cost = -1.0;
     const int64_t rows[2] = {want_dw ? N : 0, want_dx ? M : 0}, contraction[2] = {M, N};
+    constexpr int MOST = 4;  // splits of 2^0 .. 2^MOST
     for (int tn = 512; tn >= 128; tn /= 2) {
-        const double per_stage = tn == 512 ? 1170.0 : tn == 256 ? 780.0 : 585.0;
+        const double per_stage = tn == 512 ? 1300.0 : tn == 256 ? 780.0 : 585.0;
         const int64_t ct = (K + tn - 1) / tn;
         int64_t tiles[2], stages[2];
-        for (int i = 0; i < 2; ++i) {
-            tiles[i] = (rows[i] + BM - 1) / BM * ct;
-            stages[i] = (contraction[i] + BKC - 1) / BKC;
-        }
+        double unit_cost[2][MOST + 1], join_cost[2][MOST + 1];
+        int splits[2];
         auto unit = [&](int i, int split) {
             const double products = (double)((stages[i] + split - 1) / split) * per_stage;
-            const double epilogue = 18.0 * tn * (split > 1 ? 2.0 : 1.0);
+            const double epilogue = (tn == 512 ? 30.0 : 18.0) * tn * (split > 1 ? 2.0 : 1.0);
             return tn == 512 ? products + epilogue : (products > epilogue ? products : epilogue) + 1500.0;
         };
         auto join = [&](int64_t tail, int split) { return 5000.0 + (double)tail * split * (100.0 + BM * tn * 4.0 / 2500.0); };
-        auto offer = [&](double cost, const int64_t (&whole)[2], const int (&split)[2], int first) {
+        for (int i = 0; i < 2; ++i) {
+            tiles[i] = (rows[i] + BM - 1) / BM * ct;
+            stages[i] = (contraction[i] + BKC - 1) / BKC;
+            splits[i] = 1;
+            unit_cost[i][0] = unit(i, 1);
+            join_cost[i][0] = 0.0;
+            for (int k = 1; k <= MOST && tiles[i] && (tiles[i] << k) <= 4 * PAIRS && (2 << k) <= stages[i]; ++k) {
+                unit_cost[i][k] = unit(i, 1 << k);
+                join_cost[i][k] = join(tiles[i], 1 << k);
+                splits[i] = k + 1;
+            }
+        }
+        auto offer = [&](double cost, int64_t whole0, int64_t whole1, int split0, int split1, int first) {
             if (best_cost >= 0.0 && cost >= best_cost) return;
             best_cost = cost;
-            best = Plan{tn, {tiles[0], tiles[1]}, {whole[0], whole[1]}, {split[0], split[1]}, first};
+            best = LinearBwdPlan{tn, {tiles[0], tiles[1]}, {whole0, whole1}, {split0, split1}, first};
         };
-        // the last tiles of the product that goes second
-        const int first = (tiles[0] && (!tiles[1] || stages[0] >= stages[1])) ? 0 : 1, second = 1 - first;
-        const int last = tiles[second] ? second : first;
-        const int64_t total = tiles[0] + tiles[1], rest = total % PAIRS;
-        {
-            const double head = (double)((tiles[first] + PAIRS - 1) / PAIRS);
-            const double rounds = (double)((total + PAIRS - 1) / PAIRS);
-            offer(head * unit(first, 1) + (rounds - head) * unit(second, 1), tiles, {1, 1}, first);
-        }
-        int s = rest ? (int)(PAIRS / rest) : 1;
-        if (s > 16) s = 16;
-        if (s > stages[last] / 2) s = (int)(stages[last] / 2);
-        if (s >= 2 && total > rest && rest <= tiles[last]) {
-            int64_t whole[2] = {tiles[0], tiles[1]};
-            whole[last] -= rest;
-            int split[2] = {1, 1};
-            split[last] = s;
-            const int64_t n = whole[0] + whole[1];
-            const double head = (double)((whole[first] + PAIRS - 1) / PAIRS);
-            offer(head * unit(first, 1) + ((double)(n / PAIRS) - head) * unit(second, 1) + unit(last, s) + join(rest, s),
-                  whole, split, first);
-        }
-        if (total >= 2 * PAIRS) continue;
-        double unit_cost[2][5], join_cost[2][5];
-        for (int i = 0; i < 2; ++i)
-            for (int k = 0; k < 5; ++k) {
-                const bool may = k == 0 || (tiles[i] && (2 << k) <= stages[i]);
-                unit_cost[i][k] = may ? unit(i, 1 << k) : -1.0;
-                join_cost[i][k] = k ? join(tiles[i], 1 << k) : 0.0;
-            }
-        for (int a = 0; a < 5 && unit_cost[0][a] >= 0.0; ++a) {
-            for (int b = 0; b < 5 && unit_cost[1][b] >= 0.0; ++b) {
+        for (int a = 0; a < splits[0]; ++a) {
+            for (int b = 0; b < splits[1]; ++b) {
                 const int64_t n[2] = {tiles[0] << a, tiles[1] << b}, all = n[0] + n[1];
-                if (all > 4 * PAIRS) break;
-                const double u0 = unit_cost[0][a], u1 = unit_cost[1][b];
-                const int f = (n[0] && (!n[1] || u0 >= u1)) ? 0 : 1;
-                const int64_t head = (n[f] + PAIRS - 1) / PAIRS, rounds = (all + PAIRS - 1) / PAIRS;
-                offer(join_cost[0][a] + join_cost[1][b] + (double)head * (f ? u1 : u0) +
-                          (double)(rounds - head) * (f ? u0 : u1),
-                      {a ? 0 : tiles[0], b ? 0 : tiles[1]}, {1 << a, 1 << b}, f);
+                const double u[2] = {unit_cost[0][a], unit_cost[1][b]}, joins = join_cost[0][a] + join_cost[1][b];
+                const int f = (n[0] && (!n[1] || u[0] >= u[1])) ? 0 : 1;
+                const int64_t head = (n[f] + PAIRS - 1) / PAIRS;
+                auto way = [&](int64_t units) {  // of the pair with most to do, over the first `units`
+                    const int64_t rounds = (units + PAIRS - 1) / PAIRS, h = head < rounds ? head : rounds;
+                    return (double)h * u[f] + (double)(rounds - h) * u[1 - f];
+                };
+                const int64_t w0 = a ? 0 : tiles[0], w1 = b ? 0 : tiles[1];
+                offer(joins + way(all), w0, w1, 1 << a, 1 << b, f);
+                // the last tiles of the product that ends the launch, if it is whole
+                const int last = n[1 - f] ? 1 - f : f;
+                const int64_t rest = all % PAIRS;
+                if ((last ? b : a) || !rest || rest > tiles[last] || all == rest) continue;
+                int s = (int)(PAIRS / rest);
+                if (s > 16) s = 16;
+                if (s > stages[last] / 2) s = (int)(stages[last] / 2);
+                if (s < 2) continue;
+                const double extra = joins > 0.0 ? join(rest, s) - 5000.0 : join(rest, s);
+                offer(joins + way(all - rest) + unit(last, s) + extra, last ? w0 : w0 - rest, last ? w1 - rest : w1,
+                      last ? 1 << a : s, last ? s : 1 << b, f);
             }
         }
     }
     return best;
-}
-
-int64_t part_floats(const Plan& pl) {
-    return ((pl.tiles[0] - pl.whole[0]) * pl.split[0] + (pl.tiles[1] - pl.whole[1]) * pl.split[1]) * BM * pl.tn;
 }
 
 template <int TN>
@@ -521,14 +505,12 @@ int launch_products(const BwdGemmParams& p, const CUtensorMap& dy, const CUtenso
 
 }  // namespace
 
-size_t linear_backward_part_bytes(int64_t M, int64_t N, int64_t K) {
-    int64_t most = 0;
-    for (int want = 1; want < 4; ++want) {
-        const bool dw = want & 1, dx = want & 2;
-        const int64_t n = part_floats(make_plan(M, N, K, dw, dx));
-        most = n > most ? n : most;
-    }
-    return (size_t)most * 4;
+LinearBwdPlan linear_backward_plan(int64_t M, int64_t N, int64_t K, bool want_dw, bool want_dx) {
+    return make_plan(M, N, K, want_dw, want_dx);
+}
+
+size_t linear_backward_part_bytes(const LinearBwdPlan& pl) {
+    return (size_t)((pl.tiles[0] - pl.whole[0]) * pl.split[0] + (pl.tiles[1] - pl.whole[1]) * pl.split[1]) * BM * pl.tn * 4;
 }
 
 int launch_linear_backward(const LinearBwdArgs& a, cudaStream_t stream) {
@@ -538,7 +520,7 @@ int launch_linear_backward(const LinearBwdArgs& a, cudaStream_t stream) {
         return FP4ATTN_ERR_CUDA;
     int colsum_parts = 0;
     if (launch_backward_prepare(a, colsum_parts, stream) != cudaSuccess) return FP4ATTN_ERR_CUDA;
-    const Plan pl = make_plan(a.M, a.N, a.K, a.dw != nullptr, a.dx != nullptr);
+    const LinearBwdPlan& pl = a.plan;
     BwdGemmParams p{};
     p.K = (int)a.K;
     p.tn = pl.tn;
