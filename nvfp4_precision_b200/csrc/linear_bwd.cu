@@ -135,13 +135,15 @@ __device__ __forceinline__ Unit unit_of(const BwdGemmParams& p, int u) {
     return w;
 }
 
-// Which accumulator half h of a CTA's tile number `local` takes, and for the
-// how-manieth time it is taken: tiles of 512 columns take both, narrower ones
-// take turns.
+// Which accumulator half h of a CTA's tile number `local` takes: tiles of 512
+// columns take both, narrower ones take turns.  A tile that ends within its first
+// half (the last of a row of them) has no second one.
 template <int TN>
 __device__ __forceinline__ int acc_of(int local, int h) { return TN > 256 ? h : local & 1; }
 template <int TN>
-__device__ __forceinline__ int use_of(int local) { return TN > 256 ? local : local >> 1; }
+__device__ __forceinline__ int halves_of(const BwdGemmParams& p, const Unit& w) {
+    return TN > 256 && TN * w.ct + 256 < p.K ? 2 : 1;
+}
 
 template <int TN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
@@ -199,6 +201,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             const int row0 = BM * w.rt + 128 * (int)rank;
             const int col0 = TN * w.ct + C::N / 2 * (int)rank;
             const CUtensorMap* tb = a_mn ? &tm_x : &tm_w;
+            const int halves = halves_of<TN>(p, w);
             for (int ks = w.s_begin; ks < w.s_end; ++ks, ++it) {
                 const int slot = it % C::STAGES;
                 if (it >= C::STAGES &&
@@ -208,7 +211,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 }
                 if (lane == 0) {
                     // the pair's copies all count on the first CTA's barrier
-                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sm.full[slot]), 2 * C::STAGE);
+                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sm.full[slot]), 2 * (C::A_BYTES + C::B_HALF * halves));
                     const uint32_t full = mapa(smem_u32(&sm.full[slot]), 0);
                     const uint32_t at = ring_u + C::STAGE * slot;
                     const int k0 = BKC * ks;
@@ -218,10 +221,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                                          full);
 #pragma unroll
                     for (int h = 0; h < C::HALVES; ++h)
+                        if (h < halves)
 #pragma unroll
-                        for (int j = 0; j < C::N / 128; ++j)
-                            tma_load_2d_2cta(at + C::A_BYTES + C::B_HALF * h + PANEL * j, tb, col0 + C::N * h + 64 * j, k0,
-                                             full);
+                            for (int j = 0; j < C::N / 128; ++j)
+                                tma_load_2d_2cta(at + C::A_BYTES + C::B_HALF * h + PANEL * j, tb, col0 + C::N * h + 64 * j,
+                                                 k0, full);
                 }
                 __syncwarp();
             }
@@ -239,10 +243,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
                 return __all_sync(0xffffffffu, mbar_wait_spin(bar, parity, abort_flag, p.status, kLimitNs));
             };
-            int it = 0, local = 0;
+            int it = 0, local = 0, uses[2] = {0, 0};  // of the accumulators, before this unit
             bool ok = true;
             for (int u = pair; ok && u < units; u += pairs, ++local) {
                 const Unit w = unit_of(p, u);
+                const int halves = halves_of<TN>(p, w);
                 const bool a_mn = p.prod[w.which].a_mn != 0;
                 const uint32_t idesc = IDESC | (a_mn ? 1u << 15 : 0u);
                 // K-major A: 8-row groups 1 KB apart, 16 values 32 bytes on.  MN-major: 64-column
@@ -257,7 +262,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     }
 #pragma unroll
                     for (int h = 0; h < C::HALVES; ++h) {
-                        const int buf = acc_of<TN>(local, h), use = use_of<TN>(local);
+                        if (h >= halves) break;
+                        const int buf = acc_of<TN>(local, h), use = buf ? uses[1] : uses[0];
                         if (ks == w.s_begin && use > 0 && !wait(smem_u32(&sm.acc_empty[buf]), (use - 1) & 1)) {
                             ok = false;
                             break;
@@ -272,11 +278,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                                 mma_bf16_ss_2cta(tmem + 256u * buf, ad + a_step * k, bd + (2048u >> 4) * k, idesc,
                                                  (ks > w.s_begin || k > 0) ? 1u : 0u);
                             if (ks == w.s_end - 1) tc_commit_2cta(smem_u32(&sm.acc_full[buf]));
-                            if (h == C::HALVES - 1) tc_commit_2cta(smem_u32(&sm.empty[slot]));
+                            if (h == halves - 1) tc_commit_2cta(smem_u32(&sm.empty[slot]));
                         }
                         __syncwarp();
                     }
                 }
+                if (acc_of<TN>(local, 0) == 0 || halves == 2) ++uses[0];
+                if (acc_of<TN>(local, 0) == 1 || halves == 2) ++uses[1];
             }
             if (leader) {
                 tc_commit_2cta(smem_u32(&sm.final_));
@@ -290,10 +298,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int quarter = warp & 3, half = warp >> 2;
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
         const uint32_t box = ring_u + C::STAGES * C::STAGE + STORE_BOX * warp;
-        int local = 0;
+        int local = 0, uses[2] = {0, 0};
         bool ok = true;
         for (int u = pair; ok && u < units; u += pairs, ++local) {
             const Unit w = unit_of(p, u);
+            const int halves = halves_of<TN>(p, w);
             const Product& q = p.prod[w.which];
             const float g = q.g ? __ldg(q.g) : 1.0f;
             if (u == 0 && threadIdx.x == 0 && rank == 0) {
@@ -302,9 +311,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             }
             const int in_tile = 128 * (int)rank + 32 * quarter, row0 = BM * w.rt + in_tile;
 #pragma unroll 1
-            for (int h = 0; h < C::HALVES; ++h) {
+            for (int h = 0; h < halves; ++h) {
                 const int buf = acc_of<TN>(local, h);
-                if (!warp_wait(smem_u32(&sm.acc_full[buf]), use_of<TN>(local) & 1, abort_flag, p.status)) {
+                if (!warp_wait(smem_u32(&sm.acc_full[buf]), (buf ? uses[1]++ : uses[0]++) & 1, abort_flag, p.status)) {
                     ok = false;
                     break;
                 }
@@ -434,13 +443,14 @@ LinearBwdPlan make_plan(int64_t M, int64_t N, int64_t K, bool want_dw, bool want
     for (int tn = 512; tn >= 128; tn /= 2) {
         const double per_stage = tn == 512 ? 1300.0 : tn == 256 ? 780.0 : 585.0;
         const int64_t ct = (K + tn - 1) / tn;
+        const double filled = tn == 512 && (K - 1) % 512 < 256 ? ((double)ct - 0.5) / (double)ct : 1.0;
         int64_t tiles[2], stages[2];
         double unit_cost[2][MOST + 1], join_cost[2][MOST + 1];
         int splits[2];
         auto unit = [&](int i, int split) {
             const double products = (double)((stages[i] + split - 1) / split) * per_stage;
             const double epilogue = (tn == 512 ? 30.0 : 18.0) * tn * (split > 1 ? 2.0 : 1.0);
-            return tn == 512 ? products + epilogue : (products > epilogue ? products : epilogue) + 1500.0;
+            return tn == 512 ? (products + epilogue) * filled : (products > epilogue ? products : epilogue) + 1500.0;
         };
         auto join = [&](int64_t tail, int split) { return 5000.0 + (double)tail * split * (100.0 + BM * tn * 4.0 / 2500.0); };
         for (int i = 0; i < 2; ++i) {

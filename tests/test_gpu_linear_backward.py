@@ -122,3 +122,28 @@ def test_graph_replay():
     torch.cuda.synchronize()
     assert all(torch.equal(p, -q) for p, q in zip(got, want))
     assert fa.fp4attn_read_status(ws) == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(2400, 2000, 1632), (2401, 2000, 1536), (9000, 5000, 1728), (5000, 9001, 1184), (6000, 7777, 2048),
+                                   (12000, 700, 3200), (28972, 976, 928), (100, 15912, 3328), (12652, 18, 2048)])
+def test_gradients_of_large_and_uneven_products(M, N, K):
+    """Tiles of every width, whole and split, the last column's second half absent; many tiles a pair."""
+    fa = _fa()
+    gen = torch.Generator(device="cuda").manual_seed(M + N + K)
+    x = fa.fp4attn_quantize_rows(torch.randn(M, K, generator=gen, device="cuda").bfloat16(), dynamic_gscale=True)
+    w = fa.fp4attn_quantize_rows(torch.randn(N, K, generator=gen, device="cuda").bfloat16() * 0.05, dynamic_gscale=True)
+    dy = torch.randn(M, (N + 7) // 8 * 8, generator=gen, device="cuda").bfloat16()[:, :N]
+    ws = fa.new_linear_backward_workspace(M, N, K)
+    out = fa.fp4attn_linear_backward(dy, x["codes"], x["scales"], w["codes"], w["scales"], x["gscale"], w["gscale"],
+                                     workspace=ws)
+    assert fa.fp4attn_read_status(ws) == 0
+    d = dy.double()
+    # the unit-scale values are exact in fp32 (g 1), the factor g rounds once in the kernel and not here
+    for got, a, q in ((out[0], d, w), (out[1], d.t(), x)):
+        v = fa.fp4attn_dequant_rows(q["codes"], q["scales"], dtype=torch.float32).double() * q["gscale"].double()
+        _check(got, a, v)
+        del v
+    assert ref.worst(out[2], d.sum(0), d.abs().sum(0) * M * ref.U) <= 1.0
+    again = fa.fp4attn_linear_backward(dy, x["codes"], x["scales"], w["codes"], w["scales"], x["gscale"], w["gscale"],
+                                       workspace=ws)
+    assert all(torch.equal(p, q) for p, q in zip(out, again))
