@@ -407,7 +407,7 @@ typedef struct {
 } fp4attn_norm_vectors;
 
 /* Forward, in fp32 from the inputs to one rounding of each output (z from the
- * unrounded y).
+ * unrounded y; squares of values above about 1e18 leave fp32's range).
  *   x_dev : residual rows, bf16 or fp32 (x_type).  h_dev : bf16, or NULL for y = x.
  *   y_dev : x's type; may be NULL, may be x itself (of the same stride).
  *   z_dev : bf16, or NULL; or z_codes and z_scales: the NVFP4 rows of the bf16

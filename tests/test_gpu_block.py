@@ -388,3 +388,47 @@ def test_chains_through_launches_that_overlap():
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(got, want))
     assert all(fa.fp4attn_read_status(v) == 0 for v in (ws, bws, nws))
+
+
+def test_copies_and_other_streams_are_waited_for():
+    """Launches that may start early behind a kernel do not do so past a copy, a memset or an event of another stream."""
+    fa = _fa()
+    gen = _gen(21)
+    M, K, N = 3000, 1024, 512
+    w = fa.fp4attn_quantize_rows(_randn(gen, N, K, std=0.03), dynamic_gscale=True)
+    ws, nws = fa.new_linear_workspace(M, N, K), fa.new_norm_backward_workspace(M, K)
+    host = [torch.randn(M, K).to(BF).pin_memory() for _ in range(4)]
+
+    def use(x):
+        a = fa.fp4attn_linear(x, w["codes"], w["scales"], w["gscale"], workspace=ws)
+        b = fa.fp4attn_norm_gate(x, x)
+        return [a, b["y"], b["z"], fa.fp4attn_norm_gate_backward(x, None, x, x, workspace=nws)["dh"]]
+
+    want = []
+    for h in host:
+        want.append(use(h.cuda()))
+        torch.cuda.synchronize()
+    x = torch.empty(M, K, dtype=BF, device="cuda")
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        got = []
+        for h in host:  # a copy between two calls
+            x.copy_(h, non_blocking=True)
+            got.append(use(x))
+            x.zero_()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for g, v in zip(got, want) for p, q in zip(g, v))
+        got = []
+        for i, h in enumerate(host):  # another stream's work between two calls
+            done = torch.cuda.Event()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                for _ in range(20):
+                    x.copy_(host[(i + 1) % 4], non_blocking=True)
+                x.copy_(h, non_blocking=True)
+                done.record()
+            torch.cuda.current_stream().wait_event(done)
+            got.append(use(x))
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for g, v in zip(got, want) for p, q in zip(g, v))
+    assert fa.fp4attn_read_status(ws) == 0
