@@ -548,8 +548,8 @@ int launch_linear_backward(const LinearBwdArgs& a, cudaStream_t stream) {
         q.rows = (int)(dw ? a.N : a.M);
         q.contraction = (int)(dw ? a.M : a.N);
         q.a_mn = dw ? 1 : 0;
-        q.g = dw ? a.gx : a.gw;
         q.out = dw ? a.dw : a.dx;
+        q.g = !q.out ? nullptr : dw ? a.gx : a.gw;  // an absent product's scale is not read
         q.ld = dw ? a.K : a.ld_dx;
         q.row_tiles = q.out ? (q.rows + BM - 1) / BM : 0;
         q.whole = (int)pl.whole[i];

@@ -147,3 +147,21 @@ def test_gradients_of_large_and_uneven_products(M, N, K):
     again = fa.fp4attn_linear_backward(dy, x["codes"], x["scales"], w["codes"], w["scales"], x["gscale"], w["gscale"],
                                        workspace=ws)
     assert all(torch.equal(p, q) for p, q in zip(out, again))
+
+
+@pytest.mark.parametrize("M,N,K", [(64, 64, 64), (700, 264, 544), (2400, 2000, 1632)])
+def test_the_scale_of_an_absent_product_is_not_judged(M, N, K):
+    """x_gscale belongs to dw and w_gscale to dx: without the one the other may be anything."""
+    fa = _fa()
+    c = _case(M, N, K)
+    args = (c["dy"], c["x"][0], c["x"][1], c["w"][0], c["w"][1])
+    for alone, scale, other in (("want_dx", "w_gscale", "x_gscale"), ("want_dw", "x_gscale", "w_gscale")):
+        want = {k: k == alone for k in ("want_dx", "want_dw", "want_dbias")}
+        good = {scale: c["w" if scale == "w_gscale" else "x"][2]}
+        ref_out = next(t for t in fa.fp4attn_linear_backward(*args, **good, **want) if t is not None)
+        for bad in (float("nan"), 0.0, float("inf")):
+            ws = fa.new_linear_backward_workspace(M, N, K)
+            got = fa.fp4attn_linear_backward(*args, **good, **want, workspace=ws,
+                                             **{other: torch.tensor([bad], device="cuda")})
+            assert fa.fp4attn_read_status(ws) == 0
+            assert torch.equal(next(t for t in got if t is not None), ref_out)
