@@ -199,11 +199,13 @@ __device__ __forceinline__ float pivot_of(const void* row, int units) {
     }
     return 0.125f * (s.x + s.y);
 }
-// The same pivot for every CTA of a cluster.
+// The same pivots for every CTA of a cluster: each CTA's come from the team's own
+// first thread.
 template <int TPR, int MAX_K, bool WIDE>
 __device__ __forceinline__ void share_pivots(Team<TPR, MAX_K, WIDE>& team, float& p, float& q) {
     if constexpr (WIDE) {
-        float v[2] = {threadIdx.x == 0 ? p : 0.0f, threadIdx.x == 0 ? q : 0.0f};
+        const bool first = threadIdx.x % TPR == 0;
+        float v[2] = {first ? p : 0.0f, first ? q : 0.0f};
         team.sum(v);
         p = v[0] / (float)team.ranks;
         q = v[1] / (float)team.ranks;

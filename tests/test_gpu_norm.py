@@ -242,3 +242,25 @@ def test_norm_graph_and_stream():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(got, w))
+
+
+TEAMS = [104, 264, 520, 776, 1160, 1536, 2048, 2504, 4096, 5000, 6144, 7168, 8192, 10240, 12288, 16384]
+
+
+@pytest.mark.parametrize("C", TEAMS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("layer", [False, True])
+def test_equal_rows_have_equal_results(C, dtype, layer):
+    """Whichever team of a CTA takes a row: the same bits, also where the mean is many deviations off."""
+    fa = _fa()
+    gen = _gen(C)
+    M, flags = 700, fa.LAYER_NORM if layer else 0
+    v = _vectors(C, 1, gen)
+    for at in (0.5, 100.0):
+        x, h = (_rows(1, C, gen, t, at=at).repeat(M, 1) for t in (dtype, BF))
+        dz, dy = (_rows(1, C, gen, t).repeat(M, 1) for t in (BF, dtype))
+        out = fa.fp4attn_norm_gate(x, h, eps=EPS, flags=flags, **v)
+        vec = {k: t for k, t in v.items() if k != "shift"}
+        out.update(fa.fp4attn_norm_gate_backward(dz, dy, out["y"], h, eps=EPS, flags=flags, **vec))
+        for k in ("y", "z", "dx", "dh"):
+            assert (out[k] == out[k][:1]).all(), (k, at)
