@@ -104,6 +104,29 @@ __device__ __forceinline__ void tile_of(int t, int p_tiles, int q_tiles, int& pt
 
 __device__ __forceinline__ uint64_t rows_desc(uint32_t addr) { return smem_desc(addr, 16, 1024, LAYOUT_SW128); }
 
+// g_x g_w as g * pre.  Either scale may be any positive number; where their product
+// leaves fp32's normal range, pre is a power of two that brings g back into it.  A
+// sum of products is 0 or lies between 2^-20 and 2^43, so that sum * pre is exact
+// for |log2 pre| <= 64, and past that every nonzero result is outside bf16's range
+// (a zero one stays zero: g is finite).
+struct OutScale {
+    float g, pre;
+};
+__device__ __forceinline__ OutScale out_scale(float gx, float gw) {
+    const float g = __fmul_rn(gx, gw);
+    if (g >= 1.17549435e-38f && g <= 3.40282347e38f) return {g, 1.0f};
+    const double both = (double)gx * (double)gw;  // exact
+    const int e = ilogb(both);                    // of a bad scale anything: it is reported
+    const int k = e < -126 ? max(e + 126, -64) : e > 126 ? min(e - 126, 64) : 0;
+    return {fminf((float)ldexp(both, -k), 3.40282347e38f), ldexpf(1.0f, k)};
+}
+template <int W>
+__device__ __forceinline__ void prescale(uint32_t (&r)[W], float pre) {
+    if (pre != 1.0f)
+#pragma unroll
+        for (int k = 0; k < W; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * pre);
+}
+
 // Lane = column n of the output, W of its rows from m0 in one thread.
 template <int W>
 __device__ __forceinline__ void store_columns(const GemmParams& p, const uint32_t (&r)[W], float g, float bias, int n,
@@ -308,7 +331,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float gx = p.gx ? __ldcg(p.gx) : 1.0f, gw = p.gw ? __ldg(p.gw) : 1.0f;
         if (blockIdx.x == 0 && threadIdx.x == 0 && (bad_gscale(gx) || bad_gscale(gw)))
             raise_status(p.status, FP4ATTN_ERR_RANGE);
-        const float g = __fmul_rn(gx, gw);
+        const OutScale g = out_scale(gx, gw);
         const uint32_t lanes = (uint32_t)(32 * warp) << 16;
         const int row = 32 * warp + lane;
         int local = 0;
@@ -345,7 +368,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     uint32_t r[W];
                     if constexpr (W == 16) tmem_ld16(acc + c0, r); else tmem_ld32(acc + c0, r);
                     tmem_wait_ld();
-                    store_columns<W>(p, r, g, own_bias, pr, q0 + c0);
+                    prescale(r, g.pre);
+                    store_columns<W>(p, r, g.g, own_bias, pr, q0 + c0);
                     __syncwarp();
                 }
             }
@@ -360,7 +384,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         cluster_sync();
         if (warp < 4) {
             const float gx = p.gx ? __ldcg(p.gx) : 1.0f, gw = p.gw ? __ldg(p.gw) : 1.0f;
-            const float g = __fmul_rn(gx, gw);
+            const OutScale g = out_scale(gx, gw);
             int pt, qt;
             tile_of(first, p.p_tiles, p.q_tiles, pt, qt);
             const int row = threadIdx.x;  // 0..127
@@ -386,7 +410,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const int m = TN * qt + c + i;
                         if (c + i < c_end && m < p.Q &&
                             FP4ATTN_IN_BOUNDS((long long)m * p.ld + pr <= (long long)(p.Q - 1) * p.ld + p.N - 1, p.status))
-                            p.out[(long long)m * p.ld + pr] = __float2bfloat16_rn(__fmaf_rn(s[i], g, bias));
+                            p.out[(long long)m * p.ld + pr] = __float2bfloat16_rn(__fmaf_rn(s[i] * g.pre, g.g, bias));
                     }
             }
         }
@@ -563,7 +587,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
         const float gx = p.gx ? __ldcg(p.gx) : 1.0f, gw = p.gw ? __ldg(p.gw) : 1.0f;
         if (blockIdx.x == 0 && threadIdx.x == 0 && (bad_gscale(gx) || bad_gscale(gw)))
             raise_status(p.status, FP4ATTN_ERR_RANGE);
-        const float g = __fmul_rn(gx, gw);
+        const OutScale scale = out_scale(gx, gw);
+        const float g = scale.g;
         // a warp reads its quarter of the lanes and half of the columns, 64 at a time
         const int quarter = warp & 3, half = warp >> 2;
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
@@ -597,6 +622,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
                 tmem_ld32(acc + c0 + 32, r[1]);
                 tmem_wait_ld();
                 if (i == 0 && shares) report();
+                prescale(r[0], scale.pre);
+                prescale(r[1], scale.pre);
                 if constexpr (SWAP) {
                     store_columns<32>(p, r[0], g, own_bias, pr, q0);
                     store_columns<32>(p, r[1], g, own_bias, pr, q0 + 32);

@@ -247,3 +247,39 @@ def test_graph_and_stream():
         torch.cuda.synchronize()
         assert torch.equal(y, z)
     assert fa.fp4attn_read_status(ws) == 0
+
+
+# the kernel with 16, 64 and 128 columns a tile, whole and split, and the pairs with either operand on the lanes
+@pytest.mark.parametrize("M,N,K", [(3, 200, 96), (3, 200, 4128), (40, 200, 96), (40, 200, 4128), (100, 300, 288),
+                                   (100, 300, 4128), (2100, 2100, 96), (2104, 2104, 96)])
+@pytest.mark.parametrize("gx,gw,byte", [(1.3 * 2.0 ** -74, 1.7 * 2.0 ** -74, 0x7E), (1.1e24, 1.3e15, 0x01),
+                                        (2.0 ** -149, 3.0e38, 0x38), (1.9 * 2.0 ** 20, 3.1, 0x38)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_scales_whose_product_leaves_the_range(M, N, K, gx, gw, byte, bias):
+    """Each scale and each result is an ordinary number; g_x g_w in fp32 has lost its digits or is infinite."""
+    fa = _fa()
+    gen = torch.Generator(device="cuda").manual_seed(M + K)
+    gx, gw = float(np.float32(gx)), float(np.float32(gw))
+    mags = torch.tensor(ref.MAGS, device="cuda")
+    table = torch.cat([mags, -mags])
+    packed, values = [], []
+    for rows in (M, N):
+        codes = torch.randint(0, 256, (rows, K // 2), dtype=torch.uint8, device="cuda", generator=gen)
+        codes[rows // 2] = 0  # a row of zeros: its results are zero, not NaN
+        v = table[torch.stack([codes & 15, codes >> 4], -1).view(rows, K).long()]
+        packed += [codes, torch.full((-(-rows // 128) * -(-K // 64) * 512,), byte, dtype=torch.uint8, device="cuda")]
+        values.append(v * float(ref.UE4M3[byte]))
+    want = (values[0] @ values[1].t()) * (gx * gw)
+    mag = (values[0].abs() @ values[1].abs().t()) * (gx * gw)
+    b = None
+    if bias:  # of the results' size
+        b = (torch.randn(N, generator=gen, device="cuda") * float(want.std())).bfloat16()
+        want = want + b.double()
+    ws = fa.new_linear_workspace(M, N, K)
+    y = fa.fp4attn_gemm(*packed, x_gscale=torch.tensor([gx], device="cuda"), w_gscale=torch.tensor([gw], device="cuda"),
+                        bias=b, workspace=ws)
+    assert fa.fp4attn_read_status(ws) == 0 and torch.isfinite(y).all()
+    # the terms are exact in fp32: K additions and three roundings of the scales and the bias, 2^-23 each; the
+    # store by half a bf16 step, at least that of bf16's subnormals
+    bound = (mag + want.abs()) * (K + 4) * 2.0 ** -23 + want.abs() * 2.0 ** -8 + 2.0 ** -134
+    assert ((y.double() - want).abs() <= bound).all()
