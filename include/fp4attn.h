@@ -390,7 +390,7 @@ int fp4attn_linear_backward(const void* dy_bf16_dev, int64_t dy_stride, const ui
  * row strides (multiples of 8, not read for one group), e.g. slices of a
  * modulation layer's output.  NULL stands for 1, 1, 1, 0 and 0.
  * C is a multiple of 8 up to 16384, rows up to 4194304, rows a multiple of
- * groups, groups up to 1048576; eps >= 0.  Pointers are 16-byte aligned (fp32
+ * groups (0 rows: of any number, 0 too), groups up to 1048576; eps >= 0.  Pointers are 16-byte aligned (fp32
  * gradients of vectors: 4), row strides in elements, multiples of 8 (4 for
  * fp32 rows), at least C, not read for one row. */
 enum { FP4ATTN_LAYER_NORM = 8u };

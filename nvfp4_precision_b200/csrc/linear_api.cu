@@ -58,7 +58,8 @@ constexpr int64_t kMaxC = 16384;
 constexpr int64_t kMaxGroups = 1048576;
 
 int check_norm_sizes(int64_t rows, int64_t C, int64_t groups) {
-    if (rows < 0 || C <= 0 || groups <= 0 || rows % groups) return FP4ATTN_ERR_INVALID_ARG;
+    // no rows: any number of samples, none too
+    if (rows < 0 || C <= 0 || groups < 0 || (rows > 0 && (groups == 0 || rows % groups))) return FP4ATTN_ERR_INVALID_ARG;
     return (rows > kMaxRows || C % 8 || C > kMaxC || groups > kMaxGroups) ? FP4ATTN_ERR_UNSUPPORTED : FP4ATTN_OK;
 }
 // A row matrix: 16-byte aligned, rows a multiple of `unit` elements apart.

@@ -264,3 +264,23 @@ def test_equal_rows_have_equal_results(C, dtype, layer):
         out.update(fa.fp4attn_norm_gate_backward(dz, dy, out["y"], h, eps=EPS, flags=flags, **vec))
         for k in ("y", "z", "dx", "dh"):
             assert (out[k] == out[k][:1]).all(), (k, at)
+
+
+def test_an_empty_batch_of_samples():
+    """No samples at all: x [0, C] with modulation [0, C]."""
+    fa = _fa()
+    for dtype in (BF, F32):
+        x, h = torch.empty(0, 64, dtype=dtype, device="cuda"), torch.empty(0, 64, dtype=BF, device="cuda")
+        v = dict(post_weight=torch.ones(64, dtype=BF, device="cuda"), gate=h, pre_weight=None, scale=h)
+        out = fa.fp4attn_norm_gate(x, h, shift=h, **v)
+        assert out["y"].shape == out["z"].shape == (0, 64)
+        assert fa.fp4attn_norm_gate(x, h, shift=h, quantize=True, **v)["z_codes"].shape == (0, 32)
+        got = fa.fp4attn_norm_gate_backward(h, x, x, h, **v)
+        for k in ("dshift", "dscale", "dgate", "dx", "dh"):
+            assert got[k].shape == (0, 64)
+        assert (got["dpre_weight"] == 0).all() and (got["dpost_weight"] == 0).all()
+        leaf = torch.empty(0, 5, 64, dtype=dtype, device="cuda", requires_grad=True)
+        w = torch.ones(64, dtype=BF, device="cuda", requires_grad=True)
+        y, z = fa.norm_gate(leaf, torch.empty(0, 5, 64, dtype=BF, device="cuda"), w, h, None, h, h)
+        (y.float().sum() + z.float().sum()).backward()
+        assert y.shape == z.shape == leaf.grad.shape == (0, 5, 64) and (w.grad == 0).all()

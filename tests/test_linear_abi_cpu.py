@@ -154,3 +154,16 @@ def test_tensors_off_the_current_device_are_refused(fa):
         fa.norm_gate(bf, gate=bf)
     with pytest.raises(AssertionError):
         fa.fp4_linear(bf, bf.float().t())
+
+
+def test_an_empty_batch_of_samples_is_no_error(fa):
+    f = lambda **kw: fa.lib.fp4attn_norm_gate(*norm_args(fa, **kw))
+    assert f(rows=0, G=0) == fa.OK and f(rows=0, G=7) == fa.OK
+    assert f(rows=4, G=0) == fa.ERR_INVALID_ARG and f(rows=0, G=-1) == fa.ERR_INVALID_ARG
+    v = fa.NormVectors(P, P, P, 64, P, 64, P, 64)
+
+    def back(rows, G):  # no sums asked for: nothing to clear
+        return fa.lib.fp4attn_norm_gate_backward(P, 64, P, 64, P, 64, 0, P, 64, v, rows, 64, G, 1e-6, 0, P, 64, P, 64, None,
+                                                 None, None, None, None, WS, BIG, None)
+    assert back(0, 0) == fa.OK and back(4, 0) == fa.ERR_INVALID_ARG and back(0, -1) == fa.ERR_INVALID_ARG
+    assert fa.lib.fp4attn_norm_gate_backward_workspace_bytes(0, 64, 0) == 256
