@@ -302,12 +302,17 @@ PyObject* norm_gate(PyObject* const* a) {
         codes = made(x, {rows, C / 2}, at::kByte);
         scales = made(x, {scale_bytes(rows, C)}, at::kByte);
         gz = gscale_of(a[13], d);
+        require(absent(a[15]), "z is either bf16 rows or NVFP4 rows");
+    } else if (!absent(a[15])) {
+        z = tensor(a[15], "z");
     } else if (flag(a[11])) {
         z = made(x, {rows, C}, at::kBFloat16);
     }
-    const Workspace ws = workspace_of(a[15], d);
+    Rows zr{nullptr, C};
+    if (z.defined()) zr = rows_of(z, d, "z", at::kBFloat16, rows, C);
+    const Workspace ws = workspace_of(a[16], d);
     check(lib.norm_gate(xr.p, type, xr.ld, hr.p, hr.ld, &v.v, rows, C, v.count(), (float)eps, (uint32_t)flags, yr.p, yr.ld,
-                        z.defined() ? z.data_ptr() : nullptr, C, quantize ? static_cast<uint8_t*>(codes.data_ptr()) : nullptr,
+                        zr.p, zr.ld, quantize ? static_cast<uint8_t*>(codes.data_ptr()) : nullptr,
                         quantize ? static_cast<uint8_t*>(scales.data_ptr()) : nullptr, gz, ws.p, ws.bytes, d.stream()),
           "fp4attn_norm_gate");
     return quantize ? tuple_of(y, codes, scales) : tuple_of(y, z);
@@ -395,7 +400,7 @@ PyMethodDef methods[] = {
     FP4ATTN_METHOD(gemm, 9),
     FP4ATTN_METHOD(linear, 9),
     FP4ATTN_METHOD(linear_backward, 11),
-    FP4ATTN_METHOD(norm_gate, 16),
+    FP4ATTN_METHOD(norm_gate, 17),
     FP4ATTN_METHOD(norm_gate_backward, 12),
     {nullptr, nullptr, 0, nullptr},
 };

@@ -559,26 +559,27 @@ def fp4attn_norm_gate(x: torch.Tensor, h: Optional[torch.Tensor] = None, post_we
                       scale: Optional[torch.Tensor] = None, shift: Optional[torch.Tensor] = None, eps: float = 1e-6,
                       flags: int = 0, groups: Optional[int] = None, want_y: bool = True, want_z: bool = True,
                       quantize: bool = False, z_gscale: Optional[torch.Tensor] = None,
-                      y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+                      y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None,
+                      z: Optional[torch.Tensor] = None) -> dict:
     """y = x + gate * (post_weight * norm(h)) and z = norm(y) * pre_weight *
     (1 + scale) + shift, on bf16 or fp32 rows x [rows, C] and bf16 h (None for
     y = x).  RMS norms, or layer norms with flags=LAYER_NORM.  gate, scale and
     shift are bf16 [groups, C], one row for each of `groups` equal samples.
     quantize=True returns z as NVFP4 rows under the static scale z_gscale
     (None for 1), ready for fp4attn_gemm.  y may be given (x itself for an
-    update in place).  Returns dict(y, z) or dict(y, z_codes, z_scales,
-    workspace)."""
+    update in place), and z where it is not quantised.  Returns dict(y, z) or
+    dict(y, z_codes, z_scales, workspace)."""
     if stream is not None:
         return _on_stream(stream, fp4attn_norm_gate, x, h, post_weight, gate, pre_weight, scale, shift, eps, flags, groups, want_y,
-                          want_z, quantize, z_gscale, y, workspace)
+                          want_z, quantize, z_gscale, y, workspace, z=z)
     if not quantize:
         y, z = _calls.norm_gate(x, h, post_weight, gate, pre_weight, scale, shift, eps, flags, groups, want_y, want_z, False,
-                                None, y, workspace)
+                                None, y, z, workspace)
         return {"y": y, "z": z}
     if workspace is None:
         workspace = new_linear_workspace(0, 0, 32, x.device)
     y, codes, scales = _calls.norm_gate(x, h, post_weight, gate, pre_weight, scale, shift, eps, flags, groups, want_y, False,
-                                        True, z_gscale, y, workspace)
+                                        True, z_gscale, y, z, workspace)
     return dict(y=y, z_codes=codes, z_scales=scales, workspace=workspace)
 
 
@@ -640,14 +641,17 @@ class FP4LinearSTE(torch.autograd.Function):
         rows = _aligned_rows(x.reshape(-1, K))
         w = _aligned_rows(weight, 4 if weight.dtype is torch.float32 else 8)
         ws = new_linear_workspace(0, 0, 32, x.device)
+        # what is returned is no view, so that operations in place are allowed on it
+        y = x.new_empty((*x.shape[:-1], weight.shape[0]))
         qx = fp4attn_quantize_rows(rows, dynamic_gscale=True, workspace=ws)
         qw = fp4attn_quantize_rows(w, dynamic_gscale=True, workspace=ws)
-        y = fp4attn_gemm(qx["codes"], qx["scales"], qw["codes"], qw["scales"], qx["gscale"], qw["gscale"],
-                         None if bias is None else bias.to(torch.bfloat16).contiguous(), workspace=ws)
+        fp4attn_gemm(qx["codes"], qx["scales"], qw["codes"], qw["scales"], qx["gscale"], qw["gscale"],
+                     None if bias is None else bias.to(torch.bfloat16).contiguous(), y=y.view(rows.shape[0], weight.shape[0]),
+                     workspace=ws)
         _raise_status(ws, "FP4LinearSTE.forward")
         ctx.save_for_backward(qx["codes"], qx["scales"], qx["gscale"], qw["codes"], qw["scales"], qw["gscale"])
         ctx.x_shape, ctx.w_dtype, ctx.b_dtype = x.shape, weight.dtype, None if bias is None else bias.dtype
-        return y.view(*x.shape[:-1], weight.shape[0])
+        return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -687,19 +691,22 @@ class NormGate(torch.autograd.Function):
         vec = [None if t is None else _aligned_rows(t.reshape(-1, C)) for t in (gate, scale, shift)]
         one = [None if t is None else t.contiguous() for t in (post_weight, pre_weight)]
         ws = new_linear_workspace(0, 0, 32, x.device)
-        out = fp4attn_norm_gate(xr, hr, one[0], vec[0], one[1], vec[1], vec[2], eps=eps, flags=flags, groups=groups,
-                                workspace=ws)
+        # what is returned is no view, so that operations in place are allowed on it
+        y, z = x.new_empty(x.shape), x.new_empty(x.shape, dtype=torch.bfloat16)
+        fp4attn_norm_gate(xr, hr, one[0], vec[0], one[1], vec[1], vec[2], eps=eps, flags=flags, groups=groups,
+                          y=y.view(xr.shape), z=z.view(xr.shape), workspace=ws)
         _raise_status(ws, "NormGate.forward")
-        ctx.save_for_backward(out["y"], hr, one[0], vec[0], one[1], vec[1])
+        ctx.save_for_backward(y, hr, one[0], vec[0], one[1], vec[1])
         ctx.args = (eps, flags, groups if groups is not None else next((t.shape[0] for t in vec if t is not None), 1))
         ctx.like = tuple(None if t is None else (t.shape, t.dtype) for t in (x, h, post_weight, gate, pre_weight, scale, shift))
-        return out["y"].view(x.shape), out["z"].view(x.shape)
+        return y, z
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy, dz):
         _refuse_capture("NormGate")
         y, h, post_weight, gate, pre_weight, scale = ctx.saved_tensors
+        y = y.view(-1, y.shape[-1])
         eps, flags, groups = ctx.args
         dzr = torch.zeros(y.shape, dtype=torch.bfloat16, device=y.device) if dz is None else \
             _aligned_rows(dz.to(torch.bfloat16).reshape(y.shape))

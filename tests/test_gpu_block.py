@@ -432,3 +432,45 @@ def test_copies_and_other_streams_are_waited_for():
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for g, v in zip(got, want) for p, q in zip(g, v))
     assert fa.fp4attn_read_status(ws) == 0
+
+
+@pytest.mark.parametrize("lead", [(12,), (3, 4)])
+def test_results_of_the_differentiable_forms_take_operations_in_place(lead):
+    """An activation or a residual in place on what they return, and the gradients of the same out of place."""
+    fa = _fa()
+    gen = _gen(23)
+    K, N = 64, 72
+    x, r = _randn(gen, *lead, K), _randn(gen, *lead, N)
+    w = _randn(gen, N, K, std=0.1)
+    pre = _randn(gen, K)
+    grads = []
+    for inplace in (True, False):
+        leaves = [t.clone().requires_grad_() for t in (x, w, pre)]
+        a = fa.fp4_linear(leaves[0], leaves[1])
+        a = a.add_(r) if inplace else a + r
+        a = torch.nn.functional.silu(a, inplace=inplace)
+        y, z = fa.norm_gate(leaves[0], None, None, None, leaves[2])
+        z = z.mul_(2.0) if inplace else z * 2.0
+        (a.float().square().sum() + z.float().square().sum() + y.float().sum()).backward()
+        grads.append([t.grad for t in leaves] + [a.detach(), z.detach()])
+    assert all(torch.equal(p, q) for p, q in zip(*grads))
+    # y is what the backward reads: a change of it is allowed, and reported where a gradient would need the old one
+    y, z = fa.norm_gate(x.clone().requires_grad_())
+    y.add_(x)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        z.float().sum().backward()
+
+
+def test_the_norms_write_z_where_the_caller_says():
+    fa = _fa()
+    gen = _gen(26)
+    x, h = _randn(gen, 9, 64), _randn(gen, 9, 64)
+    want = fa.fp4attn_norm_gate(x, h)
+    big = torch.full((9, 80), 3.0, dtype=BF, device="cuda")
+    out = fa.fp4attn_norm_gate(x, h, z=big[:, :64], want_z=False)
+    assert out["z"].data_ptr() == big.data_ptr() and torch.equal(out["y"], want["y"])
+    assert torch.equal(big[:, :64], want["z"]) and (big[:, 64:] == 3.0).all()
+    for call in (lambda: fa.fp4attn_norm_gate(x, h, z=big), lambda: fa.fp4attn_norm_gate(x, h, z=x.float()),
+                 lambda: fa.fp4attn_norm_gate(x, h, z=x.clone(), quantize=True)):
+        with pytest.raises(AssertionError):
+            call()
