@@ -630,6 +630,14 @@ def _aligned_rows(t: torch.Tensor, unit: int = 8) -> torch.Tensor:
     return out.copy_(t)
 
 
+def _aligned_vector(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """t [n] itself, or a copy, contiguous and starting on 16 bytes (a slice of a fused bias may not)."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class FP4LinearSTE(torch.autograd.Function):
     """Training-time NVFP4 linear layer: input and weight quantised under their
     computed scales, straight-through backward."""
@@ -646,7 +654,7 @@ class FP4LinearSTE(torch.autograd.Function):
         qx = fp4attn_quantize_rows(rows, dynamic_gscale=True, workspace=ws)
         qw = fp4attn_quantize_rows(w, dynamic_gscale=True, workspace=ws)
         fp4attn_gemm(qx["codes"], qx["scales"], qw["codes"], qw["scales"], qx["gscale"], qw["gscale"],
-                     None if bias is None else bias.to(torch.bfloat16).contiguous(), y=y.view(rows.shape[0], weight.shape[0]),
+                     _aligned_vector(None if bias is None else bias.to(torch.bfloat16)), y=y.view(rows.shape[0], weight.shape[0]),
                      workspace=ws)
         _raise_status(ws, "FP4LinearSTE.forward")
         ctx.save_for_backward(qx["codes"], qx["scales"], qx["gscale"], qw["codes"], qw["scales"], qw["gscale"])
@@ -689,7 +697,7 @@ class NormGate(torch.autograd.Function):
         xr = _aligned_rows(x.reshape(-1, C), unit)
         hr = None if h is None else _aligned_rows(h.reshape(-1, C))
         vec = [None if t is None else _aligned_rows(t.reshape(-1, C)) for t in (gate, scale, shift)]
-        one = [None if t is None else t.contiguous() for t in (post_weight, pre_weight)]
+        one = [_aligned_vector(t) for t in (post_weight, pre_weight)]
         ws = new_linear_workspace(0, 0, 32, x.device)
         # what is returned is no view, so that operations in place are allowed on it
         y, z = x.new_empty(x.shape), x.new_empty(x.shape, dtype=torch.bfloat16)

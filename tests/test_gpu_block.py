@@ -474,3 +474,24 @@ def test_the_norms_write_z_where_the_caller_says():
                  lambda: fa.fp4attn_norm_gate(x, h, z=x.clone(), quantize=True)):
         with pytest.raises(AssertionError):
             call()
+
+
+def test_differentiable_forms_take_vectors_at_any_offset():
+    """Slices of a fused bias or weight that do not start on 16 bytes."""
+    fa = _fa()
+    gen = _gen(24)
+    K, N = 96, 1003
+    x, w = _randn(gen, 5, K), _randn(gen, N, K, std=0.1)
+    for dtype in (BF, torch.float32):
+        fused = _randn(gen, 2 * N, dtype=dtype).requires_grad_()
+        y = fa.fp4_linear(x, w, fused[N:])
+        assert torch.equal(y, fa.fp4_linear(x, w, fused[N:].detach().clone()))
+        y.backward(_randn(gen, 5, N))
+        assert (fused.grad[:N] == 0).all() and fused.grad[N:].abs().sum() > 0
+    fused = _randn(gen, 2 * K + 3).requires_grad_()
+    post, pre = fused[1:K + 1], fused[K + 3:]
+    got = fa.norm_gate(x, x, post, None, pre)
+    want = fa.norm_gate(x, x, post.detach().clone(), None, pre.detach().clone())
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    got[1].float().sum().backward()
+    assert fused.grad[1:].abs().sum() > 0 and fused.grad[0] == 0
