@@ -44,7 +44,12 @@ const at::Tensor& tensor(PyObject* o, const char* what) {
     return THPVariable_Unpack(o);
 }
 bool absent(PyObject* o) { return o == Py_None; }
-bool flag(PyObject* o) { return PyObject_IsTrue(o) == 1; }
+struct Failed {};  // a Python exception is set
+bool flag(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Failed{};
+    return v == 1;
+}
 
 // The current device, which every tensor of a call has to be on: the library
 // launches there, one elsewhere would be reached by address only.
@@ -161,7 +166,6 @@ Vectors vectors_of(PyObject* post, PyObject* gate, PyObject* pre, PyObject* scal
     return v;
 }
 
-struct Failed {};
 void check(int status, const char* where) {
     if (status == FP4ATTN_OK) return;
     PyObject* e = PyObject_CallFunction(error_class, "is", status, where);

@@ -495,3 +495,13 @@ def test_differentiable_forms_take_vectors_at_any_offset():
     assert all(torch.equal(p, q) for p, q in zip(got, want))
     got[1].float().sum().backward()
     assert fused.grad[1:].abs().sum() > 0 and fused.grad[0] == 0
+
+
+def test_an_argument_without_a_truth_value_is_refused():
+    fa = _fa()
+    x = torch.ones(4, 64, dtype=BF, device="cuda")
+    two = torch.zeros(2, device="cuda")
+    for call in (lambda: fa.fp4attn_quantize_rows(x, dynamic_gscale=two),
+                 lambda: fa.fp4attn_norm_gate(x, want_z=two)):
+        with pytest.raises(RuntimeError, match="ambiguous"):
+            call()
