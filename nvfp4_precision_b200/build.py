@@ -25,9 +25,16 @@ LIB = os.path.join(PKG, "libfp4attn.so")
 # build; the binding loads it when FP4ATTN_BOUNDS_CHECK=1.
 LIB_CHECKED = os.path.join(PKG, "libfp4attn_checked.so")
 
-# The calls of the linear layers and norms from Python (csrc/calls.cpp).
-CALLS = os.path.join(PKG, "_calls.so")
 CALLS_SRC = os.path.join(CSRC, "calls.cpp")
+
+
+def calls_path() -> str:
+    """The extension with the calls of the linear layers and norms from Python
+    (csrc/calls.cpp).  It holds for one Python and one torch, which its name
+    tells: after a change of either it is not there until it is built again."""
+    import torch
+    return os.path.join(PKG, f"_calls.{sys.implementation.cache_tag}.torch-{torch.__version__}.so")
+
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -42,25 +49,25 @@ def sources():
 
 
 def build_calls(force: bool = False) -> str:
+    out = calls_path()
     deps = [CALLS_SRC, os.path.join(INCLUDE, "fp4attn.h")]
-    if not force and os.path.exists(CALLS) and all(os.path.getmtime(CALLS) >= os.path.getmtime(d) for d in deps):
-        return CALLS
+    if not force and os.path.exists(out) and all(os.path.getmtime(out) >= os.path.getmtime(d) for d in deps):
+        return out
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
-    tmp = CALLS + f".tmp{os.getpid()}"
+    tmp = out + f".tmp{os.getpid()}"
     includes = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
                 os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
                     f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{i}" for i in includes),
                     CALLS_SRC, f"-L{root}/lib", f"-Wl,-rpath,{root}/lib", "-ltorch_python", "-ltorch", "-ltorch_cpu",
                     "-lc10", "-lc10_cuda", "-o", tmp], check=True)
-    os.replace(tmp, CALLS)
-    return CALLS
+    os.replace(tmp, out)
+    return out
 
 
-def build(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
-    build_calls(force and not checked)
+def build_library(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
     out = LIB_CHECKED if checked else LIB
     deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) \
         + glob.glob(os.path.join(INCLUDE, "*.h"))
@@ -76,6 +83,13 @@ def build(force: bool = False, verbose: bool = False, checked: bool = False) -> 
     cmd += [*sources(), "-o", tmp]
     subprocess.run(cmd, check=True)
     os.replace(tmp, out)
+    return out
+
+
+def build(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
+    # the library first: the attention does not need the extension
+    out = build_library(force, verbose, checked)
+    build_calls(force and not checked)
     return out
 
 

@@ -2,16 +2,21 @@
 
 Argument marshalling only: every step of the path runs in the library's
 kernels.  torch supplies device memory and the current stream.  Importing
-this module loads ``libfp4attn.so`` and raises if it is missing -- there is
+this module loads ``libfp4attn.so`` and raises if it is missing, the first
+call of a linear layer or norm does the same with their extension -- there is
 no fallback implementation.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 from typing import Optional
 
 import torch
+
+from . import build
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # FP4ATTN_BOUNDS_CHECK=1 selects the bounds-checked build of the same library
@@ -417,17 +422,29 @@ def fp4_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, softmax_sca
 # checks, outputs and library calls are made in native code (csrc/calls.cpp).
 
 def _load_calls():
-    path = os.path.join(_PKG, "_calls.so")
+    path = build.calls_path()
     if not os.path.exists(path):
         raise ImportError(f"extension {path} is missing; build it with `python -m nvfp4_precision_b200.build`")
-    from . import _calls
-    _calls.bind(Fp4AttnError, *(ctypes.cast(getattr(lib, "fp4attn_" + n), ctypes.c_void_p).value
+    name = __package__ + "._calls"
+    loader = importlib.machinery.ExtensionFileLoader(name, path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_file_location(name, path, loader=loader))
+    loader.exec_module(module)
+    module.bind(Fp4AttnError, *(ctypes.cast(getattr(lib, "fp4attn_" + n), ctypes.c_void_p).value
                                 for n in ("quantize_rows", "dequant_rows", "gemm", "linear", "linear_backward", "norm_gate",
                                           "norm_gate_backward")))
-    return _calls
+    return module
 
 
-_calls = _load_calls()
+class _Unloaded:
+    """Stands for the extension until its first call: the attention does without it."""
+
+    def __getattr__(self, name):
+        global _calls
+        _calls = _load_calls()
+        return getattr(_calls, name)
+
+
+_calls = _Unloaded()
 
 
 def _on_stream(stream, fn, *args, **kwargs):
