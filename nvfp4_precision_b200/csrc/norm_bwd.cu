@@ -254,7 +254,9 @@ __global__ void __launch_bounds__(THREADS, 1) norm_gate_bwd_kernel(const __grid_
                 moments();
             }
             // n = y r - mean r and the like: the products' roundings are of the size
-            // of the mean's own.  dx = dy + r dn - r c1 n - r mean(dn)
+            // of the mean's own.  dx = dy + r dn - r c1 n - r mean(dn); the layer norm
+            // adds its three terms first, so that a large dy is rounded once (for the RMS
+            // norm's two, added to dy one after the other, that would be one more step)
             float2 dm[J][P];
             float2 s_dmm = both(0.0f), s_dm = both(0.0f);
             const float2 ry2 = both(ry), rh2 = both(rh), my2 = both(-mean_y * ry), mh2 = both(-mean_h * rh),
@@ -282,9 +284,11 @@ __global__ void __launch_bounds__(THREADS, 1) norm_gate_bwd_kernel(const __grid_
                         const float2 m = LAYER ? __ffma2_rn(f[i], rh2, mh2) : __fmul2_rn(f[i], rh2);
                         s_dz[j][i] = __fadd2_rn(s_dz[j][i], d[i]);
                         s_dzn[j][i] = __ffma2_rn(d[i], n, s_dzn[j][i]);
-                        if (LAYER) g[i] = __fadd2_rn(g[i], md2);
-                        g[i] = __ffma2_rn(n, c12, g[i]);
-                        g[i] = __ffma2_rn(__fmul2_rn(d[i], B[i]), ry2, g[i]);  // dx
+                        const float2 dn = __fmul2_rn(d[i], B[i]);
+                        if constexpr (LAYER)
+                            g[i] = __fadd2_rn(g[i], __ffma2_rn(dn, ry2, __ffma2_rn(n, c12, md2)));  // dx
+                        else
+                            g[i] = __ffma2_rn(dn, ry2, __ffma2_rn(n, c12, g[i]));
                         s_dxm[j][i] = __ffma2_rn(g[i], m, s_dxm[j][i]);
                         dm[j][i] = __fmul2_rn(g[i], A[i]);
                         s_dmm = __ffma2_rn(dm[j][i], m, s_dmm);

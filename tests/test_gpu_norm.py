@@ -284,3 +284,38 @@ def test_an_empty_batch_of_samples():
         y, z = fa.norm_gate(leaf, torch.empty(0, 5, 64, dtype=BF, device="cuda"), w, h, None, h, h)
         (y.float().sum() + z.float().sum()).backward()
         assert y.shape == z.shape == leaf.grad.shape == (0, 5, 64) and (w.grad == 0).all()
+
+
+def _off_centre(M, C, gen, dtype, kind):
+    """Rows whose moments lose bits about 0 or about a few of their own values."""
+    if kind == "pivot":  # outliers where the kernels look for a first guess of the mean, in each CTA's columns
+        x = torch.randn(M, C, generator=gen, device="cuda")
+        ctas = -(-C // 6144)
+        cols = C if ctas == 1 else -(-C // (64 * ctas)) * 64
+        for r in range(ctas):
+            mid = cols * r + (min(cols, C - cols * r) // 2)
+            x[:, max(mid - 8, 0):mid + 8] += 300.0
+        return x.to(dtype)
+    return (float(kind) + torch.randn(M, C, generator=gen, device="cuda")).to(dtype)
+
+
+@pytest.mark.parametrize("C", TEAMS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("kind", ["pivot", 10, -1000])
+def test_layer_norm_of_rows_far_from_zero(C, dtype, kind):
+    fa = _fa()
+    gen = _gen(C + 7)
+    M = 37
+    x, h = _off_centre(M, C, gen, dtype, kind), _off_centre(M, C, gen, BF, kind)
+    v = _vectors(C, 1, gen)
+    out = fa.fp4attn_norm_gate(x, h, eps=EPS, flags=fa.LAYER_NORM, **v)
+    want, bound = ref.norm_gate64(x, h, v["post_weight"], v["gate"], v["pre_weight"], v["scale"], v["shift"], 1, True, EPS)
+    for k in ("y", "z"):
+        assert ref.worst(out[k], want[k], bound[k]) <= 1.0, k
+    dz, dy = _rows(M, C, gen), _rows(M, C, gen, dtype)
+    vec = {k: t for k, t in v.items() if k != "shift"}
+    got = fa.fp4attn_norm_gate_backward(dz, dy, out["y"], h, eps=EPS, flags=fa.LAYER_NORM, **vec)
+    want, bound = ref.norm_gate_backward64(dz, dy, out["y"], h, v["post_weight"], v["gate"], v["pre_weight"], v["scale"], 1,
+                                           True, EPS)
+    for k in want:
+        assert ref.worst(got[k], want[k], bound[k]) <= 1.0, k
