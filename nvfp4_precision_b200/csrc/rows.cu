@@ -144,10 +144,13 @@ __global__ void __launch_bounds__(Q_THREADS, 1) quantize_rows_kernel(const __gri
     __shared__ float scratch[Q_CONSUMERS / 32];
     __shared__ int abort_all;
     // Behind the pass for the maxima, which has waited for whatever writes x, x
-    // may be loaded at once: only the maxima themselves are waited for.
+    // may be loaded at once: only the maxima themselves are waited for, by the
+    // threads that read them.
     const bool behind_maxima = a.n_part > 0;
-    if (!behind_maxima) pdl_wait();
-    pdl_trigger();
+    if (!behind_maxima) {
+        pdl_wait();
+        pdl_trigger();
+    }
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int chunks = (int)scale_chunks(a.K), units_wide = (chunks + 1) / 2;
@@ -204,6 +207,7 @@ __global__ void __launch_bounds__(Q_THREADS, 1) quantize_rows_kernel(const __gri
             float m = 0.0f;
             if (behind_maxima) {
                 pdl_wait();
+                pdl_trigger();
                 for (int i = t; i < a.n_part; i += Q_CONSUMERS) m = max_nan(m, __ldcg(a.part + i));
             } else {
                 const int64_t per_row = a.K / 16;
