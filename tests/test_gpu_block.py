@@ -505,3 +505,35 @@ def test_an_argument_without_a_truth_value_is_refused():
                  lambda: fa.fp4attn_norm_gate(x, want_z=two)):
         with pytest.raises(RuntimeError, match="ambiguous"):
             call()
+
+
+def test_every_call_on_a_stream_that_is_named():
+    """stream= gives the results of the current stream."""
+    fa = _fa()
+    gen = _gen(25)
+    M, K, N, G = 60, 96, 40, 3
+    x, h, dy = _randn(gen, M, K), _randn(gen, M, K), _randn(gen, M, N)
+    wt = _randn(gen, N, K, std=0.1)
+    v = dict(zip(("post_weight", "pre_weight"), _randn(gen, 2, K)), **dict(zip(("gate", "scale", "shift"), _randn(gen, 3, G, K))))
+    bias, g = _randn(gen, N), torch.tensor([0.02], device="cuda")
+
+    def every(**kw):
+        w = fa.fp4attn_quantize_rows(wt, dynamic_gscale=True, **kw)
+        q = fa.fp4attn_quantize_rows(x, g, **kw)
+        packed, gs = (q["codes"], q["scales"], w["codes"], w["scales"]), (g, w["gscale"])
+        n = fa.fp4attn_norm_gate(x, h, groups=G, eps=1e-3, flags=fa.LAYER_NORM, **v, **kw)
+        nq = fa.fp4attn_norm_gate(x, h, quantize=True, z_gscale=g, want_y=False, **v, **kw)
+        back = {k: t for k, t in v.items() if k != "shift"}
+        b = fa.fp4attn_norm_gate_backward(x, h, n["y"], h, groups=G, eps=1e-3, flags=fa.LAYER_NORM, **back, **kw)
+        # scale bytes of rows that do not exist are not the norm's to write
+        return [q["codes"], fa.fp4attn_dequant_rows(q["codes"], q["scales"], g, torch.float32, **kw),
+                fa.fp4attn_gemm(*packed, *gs, bias, **kw), fa.fp4attn_linear(x, *packed[2:], gs[1], g, bias=bias, **kw),
+                *fa.fp4attn_linear_backward(dy, *packed, *gs, **kw), n["y"], n["z"], nq["z_codes"], *b.values()]
+
+    want = every()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for name in (s, s.cuda_stream):
+        got = every(stream=name)
+        s.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want))

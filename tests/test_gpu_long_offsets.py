@@ -141,3 +141,56 @@ def test_norm_and_its_gradients(layer, dtype):
             # the period's bound counts PERIOD + 16 roundings of its sum; here they are ROWS + 16
             grown = bound[k] * TIMES * (ROWS + 16) / (PERIOD + 16)
             assert ref.worst(out[k], want[k] * TIMES, grown) <= 1.0, k
+
+
+@pytest.mark.parametrize("layer", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_column_sums_miss_no_row(layer, dtype):
+    """The norms' sums down ROWS rows to less than the rows beyond 2^31 elements add to them.
+
+    dshift sums small integers: exact.  The others: a CTA of this width is one team, which adds the rows of a
+    part one after the other; the parts (their number shows in the workspace's size) are added in order."""
+    fa = _fa()
+    gen, C, flags = _gen(4), WIDE, fa.LAYER_NORM if layer else 0
+    rows = lambda t=torch.bfloat16: torch.randn(PERIOD, C, device="cuda", generator=gen).to(t)
+    vec = lambda: (1.0 + 0.1 * torch.randn(C, device="cuda", generator=gen)).bfloat16()
+    mod = lambda: (0.3 * torch.randn(1, C, device="cuda", generator=gen)).bfloat16()
+    v = dict(post_weight=vec(), gate=mod(), pre_weight=vec(), scale=mod())
+    y, h, dy = rows(dtype), rows(), rows(dtype)
+    dz = torch.randint(-1, 2, (PERIOD, C), device="cuda", generator=gen).bfloat16()
+    work = fa.new_norm_backward_workspace(ROWS, C, 1)
+    parts = (work.numel() - 256) // (12 * C)
+    depth = -(-ROWS // parts) + parts + 16
+    assert 100 <= parts <= 600
+    out = fa.fp4attn_norm_gate_backward(dz.repeat(TIMES, 1), dy.repeat(TIMES, 1), y.repeat(TIMES, 1), h.repeat(TIMES, 1),
+                                        flags=flags, eps=1e-6, workspace=work, **v)
+    assert fa.fp4attn_read_status(work) == 0
+    assert torch.equal(out["dshift"], TIMES * dz.double().sum(0, keepdim=True).float())
+    want, bound = ref.norm_gate_backward64(dz, dy, y, h, v["post_weight"], v["gate"], v["pre_weight"], v["scale"], 1, layer,
+                                           1e-6)
+    beyond = 1.0 - 2 ** 31 / (ROWS * C)  # the share of a column's rows that lies there
+    for k in ("dscale", "dgate", "dpre_weight", "dpost_weight"):
+        # the period's bound counts PERIOD + 16 roundings of each term, and the terms' own errors
+        grown = bound[k] * TIMES * (depth / (PERIOD + 16))
+        assert ref.worst(out[k], want[k] * TIMES, grown) <= 1.0, k
+        # without those rows the sums would be off by more, in most columns
+        assert (want[k].abs() * TIMES * beyond > grown).double().mean() > 0.5, k
+
+
+@pytest.mark.parametrize("M,N,K", [(28972, 976, 928), (12652, 18, 2048), (100, 15912, 3328), (9000, 5000, 1728)])
+def test_long_contractions_are_whole(M, N, K):
+    """Operands whose sums are exact in fp32 in any order: every gradient has one right value."""
+    fa = _fa()
+    gen = _gen(M)
+    xc, xs, xv = _packed(M, K, gen)
+    wc, ws, wv = _packed(N, K, gen)
+    dy = torch.randint(-1, 2, (M, -(-N // 8) * 8), device="cuda", generator=gen).bfloat16()[:, :N]
+    assert 12 * max(M, N) < 2 ** 24  # halves
+    work = fa.new_linear_backward_workspace(M, N, K)
+    args = (dy, xc, xs, wc, ws)
+    d = dy.double()
+    want = ((d @ wv).bfloat16(), (d.t() @ xv).bfloat16(), d.sum(0).float())
+    for only in ((True, True, True), (True, False, False), (False, True, False)):
+        got = fa.fp4attn_linear_backward(*args, want_dx=only[0], want_dw=only[1], want_dbias=only[2], workspace=work)
+        assert fa.fp4attn_read_status(work) == 0
+        assert all(g is None or torch.equal(g, w) for g, w in zip(got, want))

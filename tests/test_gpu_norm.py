@@ -319,3 +319,24 @@ def test_layer_norm_of_rows_far_from_zero(C, dtype, kind):
                                            True, EPS)
     for k in want:
         assert ref.worst(got[k], want[k], bound[k]) <= 1.0, k
+
+
+@pytest.mark.parametrize("M,C,G", [(1, 32, 1), (1, 6144, 1), (130, 96, 2), (64, 256, 4), (500, 544, 1), (90, 768, 3),
+                                   (257, 1056, 1), (70, 1536, 1), (300, 2080, 3), (200, 2048, 2), (60, 4096, 1),
+                                   (129, 4128, 1), (1000, 6144, 2), (33, 8192, 1), (16, 12288, 1), (5, 16384, 5)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_quantised_layer_norm_is_the_quantiser_of_z(M, C, G, dtype):
+    fa = _fa()
+    gen = _gen(M * 5 + C)
+    x, h = _rows(M, C, gen, dtype, at=0.5, std=3.0), _rows(M, C, gen)
+    v = _vectors(C, G, gen)
+    g = torch.tensor([0.013], device="cuda")
+    for gz in (None, g):
+        for hh in (h, None):
+            vec = v if hh is not None else {**v, "gate": None, "post_weight": None}
+            z = fa.fp4attn_norm_gate(x, hh, eps=EPS, flags=fa.LAYER_NORM, **vec)
+            q = fa.fp4attn_norm_gate(x, hh, eps=EPS, flags=fa.LAYER_NORM, quantize=True, z_gscale=gz, **vec)
+            want = fa.fp4attn_quantize_rows(z["z"], gscale=gz)
+            assert torch.equal(q["y"], z["y"]) and torch.equal(q["z_codes"], want["codes"])
+            assert torch.equal(fa.untile_scales(q["z_scales"], M, C), fa.untile_scales(want["scales"], M, C))
+            assert fa.fp4attn_read_status(q["workspace"]) == 0
