@@ -24,7 +24,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) norm_gate_kernel(const __grid_
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t bars[TEAMS * MAX_SLOTS];
     __shared__ __align__(16) float scratch[TEAMS * TeamT::SCRATCH];
-    __shared__ uint64_t team_bars[TEAMS];
+    __shared__ uint64_t team_bars[2 * TEAMS];
     __shared__ int abort_all;
     __shared__ ScaleTable table;  // not used (and not there) unless QUANT
     const int t = threadIdx.x % TPR;
@@ -34,8 +34,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) norm_gate_kernel(const __grid_
     team.phase = 0;
     team.rank = WIDE ? cluster_ctarank() : 0;
     team.ranks = WIDE ? cluster_nctarank() : 1;
-    team.bar = smem_u32(&team_bars[team.index]);
-    team.parity = 0;
+    team.bars = smem_u32(&team_bars[2 * team.index]);
+    team.turn = 0;
     team.abort_flag = &abort_all;
     team.status = a.status;
     const int c0 = first_column(a.cols, team.rank), cols = min(a.cols, a.C - c0), NU = cols / U;
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) norm_gate_kernel(const __grid_
     if (threadIdx.x == 0) abort_all = 0;
     for (int i = threadIdx.x; i < TEAMS * MAX_SLOTS; i += blockDim.x) mbar_init(smem_u32(&bars[i]), 1);
     for (int i = threadIdx.x; i < (int)(sizeof(scratch) / 4); i += blockDim.x) scratch[i] = 0.0f;
-    if (WIDE && threadIdx.x < TEAMS) mbar_init(smem_u32(&team_bars[threadIdx.x]), team.ranks * TeamT::warps);
+    if (WIDE && threadIdx.x < 2 * TEAMS) mbar_init(smem_u32(&team_bars[threadIdx.x]), team.ranks * TeamT::warps);
     fence_mbar_init();
     __syncthreads();
     if constexpr (WIDE) cluster_sync();

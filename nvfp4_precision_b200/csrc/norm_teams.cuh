@@ -99,7 +99,11 @@ __device__ __forceinline__ void load_vector(const __nv_bfloat16* p, int64_t at, 
 // What a thread knows of its team: TPR threads of the CTA, or (WIDE) of each CTA of
 // the cluster.  Sums of up to MAX_K quantities.  A wide team's warps write their
 // sums into every CTA and arrive on a barrier there: several teams of a cluster
-// go their own ways, and a row costs no barrier over all of it.
+// go their own ways, and a row costs no barrier over all of it.  Two barriers take
+// turns: a warp that has met the others at its own CTA's barrier knows nothing of
+// another CTA's, where arrivals of the same turn may still be under way, so its next
+// arrival there must not count for them.  At the turn after that it may: everyone has
+// arrived for the one between, and did so behind the first.
 template <int TPR, int MAX_K, bool WIDE>
 struct Team {
     static constexpr int warps = TPR / 32;
@@ -109,8 +113,9 @@ struct Team {
     float* scratch;
     int index, phase;
     uint32_t rank, ranks;
-    // WIDE: this team's barrier (ranks * warps arrivals), and what a wait needs
-    uint32_t bar, parity;
+    // WIDE: this team's two barriers (ranks * warps arrivals), the turns so far, and
+    // what a wait needs
+    uint32_t bars, turn;
     volatile int* abort_flag;
     int* status;
 
@@ -118,9 +123,10 @@ struct Team {
     __device__ __forceinline__ void arrive_and_wait() {
         __syncwarp();
         const int lane = threadIdx.x & 31;
+        const uint32_t bar = bars + 8u * (turn & 1);
         if (lane < (int)ranks) mbar_arrive_cluster(mapa(bar, (uint32_t)lane));
-        mbar_wait_cluster(bar, parity, abort_flag, status, kLimitNs);
-        parity ^= 1;
+        mbar_wait_cluster(bar, (turn >> 1) & 1, abort_flag, status, kLimitNs);
+        ++turn;
     }
 
     __device__ __forceinline__ void sync() {

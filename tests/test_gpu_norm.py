@@ -340,3 +340,25 @@ def test_quantised_layer_norm_is_the_quantiser_of_z(M, C, G, dtype):
             assert torch.equal(q["y"], z["y"]) and torch.equal(q["z_codes"], want["codes"])
             assert torch.equal(fa.untile_scales(q["z_scales"], M, C), fa.untile_scales(want["scales"], M, C))
             assert fa.fp4attn_read_status(q["workspace"]) == 0
+
+
+@pytest.mark.parametrize("C", [8192, 16384])
+@pytest.mark.parametrize("layer", [False, True])
+@pytest.mark.parametrize("branch", [False, True])
+def test_clusters_meet_row_after_row(C, layer, branch):
+    """Rows shared by two and three CTAs, thousands of meetings on the same barriers, every row known."""
+    fa = _fa()
+    gen = _gen(C + 1)
+    M, period, flags = 7777, 11, fa.LAYER_NORM if layer else 0
+    at = torch.arange(M, device="cuda") % period
+    x, h, dz, dy = (_rows(period, C, gen, at=0.5) for _ in range(4))
+    h = h if branch else None
+    one = fa.fp4attn_norm_gate(x, h, eps=EPS, flags=flags)
+    few = fa.fp4attn_norm_gate_backward(dz, dy, one["y"], h, eps=EPS, flags=flags)
+    ws, nws = fa.new_linear_workspace(0, 0, 32), fa.new_norm_backward_workspace(M, C)
+    big = lambda t: None if t is None else t[at].contiguous()
+    out = fa.fp4attn_norm_gate(big(x), big(h), eps=EPS, flags=flags, workspace=ws)
+    got = fa.fp4attn_norm_gate_backward(big(dz), big(dy), out["y"], big(h), eps=EPS, flags=flags, workspace=nws)
+    assert torch.equal(out["y"], big(one["y"])) and torch.equal(out["z"], big(one["z"]))
+    assert torch.equal(got["dx"], big(few["dx"])) and (not branch or torch.equal(got["dh"], big(few["dh"])))
+    assert fa.fp4attn_read_status(ws) == 0 and fa.fp4attn_read_status(nws) == 0
