@@ -246,7 +246,8 @@ int shape_of(const void* kernel, const Split& s, size_t fixed_bytes, size_t slot
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh.smem) != cudaSuccess)
+        // the same for every size: another thread may set it between this and the launch
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES) != cudaSuccess)
         return FP4ATTN_ERR_CUDA;
     int64_t clusters = sms / s.ctas;
     if (s.ctas > 1) {

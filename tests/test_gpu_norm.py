@@ -362,3 +362,43 @@ def test_clusters_meet_row_after_row(C, layer, branch):
     assert torch.equal(out["y"], big(one["y"])) and torch.equal(out["z"], big(one["z"]))
     assert torch.equal(got["dx"], big(few["dx"])) and (not branch or torch.equal(got["dh"], big(few["dh"])))
     assert fa.fp4attn_read_status(ws) == 0 and fa.fp4attn_read_status(nws) == 0
+
+
+def test_calls_of_several_threads():
+    """The C entry points from threads of their own, on streams and rows of their own: each call is accepted."""
+    import threading
+    fa = _fa()
+    gen = _gen(30)
+    shapes = [(3, 4352), (2, 6144), (5, 5000), (4, 4608)]
+    wrong, start = [], threading.Barrier(len(shapes))
+
+    def work(M, C, s):
+        x, h, z, dx, dh, want = s["t"]
+        vec, ws, stream = fa.NormVectors(), s["ws"], s["stream"].cuda_stream
+        start.wait()
+        for _ in range(1500):
+            rc = fa.lib.fp4attn_norm_gate(x.data_ptr(), fa.BF16, C, h.data_ptr(), C, vec, M, C, 1, EPS, 0, None, 0,
+                                          z.data_ptr(), C, None, None, None, None, 0, stream)
+            rc = rc or fa.lib.fp4attn_norm_gate_backward(z.data_ptr(), C, None, 0, x.data_ptr(), C, fa.BF16, h.data_ptr(), C, vec,
+                                                         M, C, 1, EPS, 0, dx.data_ptr(), C, dh.data_ptr(), C, None, None, None,
+                                                         None, None, ws.data_ptr(), ws.numel(), stream)
+            if rc:
+                wrong.append((C, rc))
+                return
+
+    state = []
+    for M, C in shapes:
+        x, h = _rows(M, C, gen), _rows(M, C, gen)
+        want = fa.fp4attn_norm_gate(x, h, eps=EPS)["z"]
+        state.append(dict(t=(x, h, torch.empty_like(x), torch.empty_like(x), torch.empty_like(x), want),
+                          ws=fa.new_norm_backward_workspace(M, C), stream=torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(M, C, s)) for (M, C), s in zip(shapes, state)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not wrong, wrong
+    for s in state:
+        assert torch.equal(s["t"][2], s["t"][5]) and fa.fp4attn_read_status(s["ws"]) == 0
