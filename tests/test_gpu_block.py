@@ -537,3 +537,40 @@ def test_every_call_on_a_stream_that_is_named():
         got = every(stream=name)
         s.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+def test_large_and_wide_calls_captured():
+    """Launches of clusters and pairs in a graph, replayed on other inputs: large products, rows of two and three CTAs."""
+    fa = _fa()
+    gen = _gen(27)
+    M, N, K = 2104, 2096, 544
+    w = fa.fp4attn_quantize_rows(_randn(gen, N, K, std=0.05), dynamic_gscale=True)
+    ws, bws = fa.new_linear_workspace(M, N, K), fa.new_linear_backward_workspace(M, N, K)
+    wide = [(60, 8192), (40, 16384)]
+    nws = [fa.new_norm_backward_workspace(*s) for s in wide]
+    sources = [[_randn(gen, M, K), _randn(gen, M, N)] + [_randn(gen, *s) for s in wide] for _ in range(2)]
+
+    def every(x, dy, *rows):
+        q = fa.fp4attn_quantize_rows(x, dynamic_gscale=True, workspace=ws)
+        packed = (q["codes"], q["scales"], w["codes"], w["scales"])
+        out = [fa.fp4attn_gemm(*packed, q["gscale"], w["gscale"], workspace=ws),
+               fa.fp4attn_linear(x[:5], *packed[2:], w["gscale"], dynamic_gscale=True, workspace=ws),
+               *fa.fp4attn_linear_backward(dy, *packed, q["gscale"], w["gscale"], workspace=bws)]
+        for r, b in zip(rows, nws):
+            n = fa.fp4attn_norm_gate(r, r, flags=fa.LAYER_NORM)
+            out += [n["y"], n["z"], *fa.fp4attn_norm_gate_backward(r, r, n["y"], r, flags=fa.LAYER_NORM, workspace=b).values()]
+        return out
+
+    want = [[t.clone() for t in every(*s)] for s in sources]
+    held = [t.clone() for t in sources[0]]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = every(*held)
+    for s, v in ((sources[1], want[1]), (sources[0], want[0])):
+        for t, u in zip(held, s):
+            t.copy_(u)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, v))
+    assert all(fa.fp4attn_read_status(t) == 0 for t in (ws, bws, *nws))

@@ -283,3 +283,19 @@ def test_scales_whose_product_leaves_the_range(M, N, K, gx, gw, byte, bias):
     # store by half a bf16 step, at least that of bf16's subnormals
     bound = (mag + want.abs()) * (K + 4) * 2.0 ** -23 + want.abs() * 2.0 ** -8 + 2.0 ** -134
     assert ((y.double() - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 200, 4128), (40, 200, 4128), (100, 300, 4128), (2100, 2100, 288), (2104, 2101, 288)])
+def test_scale_bytes_of_rows_past_the_end_do_not_matter_to_any_kernel(M, N, K):
+    """As above, for split products and for pairs with either operand on the lanes."""
+    fa = _fa()
+    _, xc, xs, xg = ref.make_packed(M, K, 1)
+    _, wc, ws_, wg = ref.make_packed(N, K, 2)
+    x, w = ref.packed_to("cuda", xc, xs, xg), ref.packed_to("cuda", wc, ws_, wg)
+    y = fa.fp4attn_gemm(x[0], x[1], w[0], w[1], x_gscale=x[2], w_gscale=w[2])
+    for p, rows in ((x, M), (w, N)):
+        R, C = -(-rows // 128), -(-K // 64)
+        t = p[1].view(R, C, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(R * 128, C * 4).clone()
+        t[rows:] = 0x7F
+        p[1].copy_(t.view(R, 4, 32, C, 4).permute(0, 3, 2, 1, 4).reshape(-1))
+    assert torch.equal(y, fa.fp4attn_gemm(x[0], x[1], w[0], w[1], x_gscale=x[2], w_gscale=w[2]))
