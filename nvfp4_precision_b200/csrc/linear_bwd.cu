@@ -43,7 +43,7 @@ constexpr int WARP_PRODUCER = STORE_WARPS, WARP_MMA = STORE_WARPS + 1;
 constexpr uint32_t PANEL = 64 * 128;  // 64 rows of 64 bf16
 constexpr uint64_t kLimitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
-constexpr int PAIRS = 74;  // of 148 SMs
+constexpr int PAIRS = 74;  // of 148 SMs; with fewer, plans made for these are slower, not wrong
 
 template <int TN>
 struct Cfg {

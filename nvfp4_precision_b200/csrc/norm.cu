@@ -15,8 +15,12 @@ namespace {
 // reductions and the quantiser behind.
 
 // FULL: the row fills its team, no thread is left without channels.  The quantised
-// forms, which instructions bound, have it: layer norm, 36864 x 6144, 381 -> 350 us
-// (without quantisation the same within 2%).
+// forms have it (without quantisation the same within 2%), for teams of 128 and 256
+// threads.  Without and with it, layer norm of bf16 and fp32 rows, RMS norm of both:
+//   36864 x 6144   373 -> 344, 485 -> 476, 307 -> 295, 440 -> 406 us
+//   55296 x 4096   412 -> 373, 535 -> 522, 336 -> 322, 477 -> 453
+// Narrower teams have no such instances: bf16 rows would gain 10 to 16% (147456 x
+// 1536: 330 -> 289 us), fp32 RMS norms lose at some widths (294912 x 768: 403 -> 434).
 template <int TPR, int J, int U, bool LAYER, bool QUANT, bool WIDE, bool FULL>
 __global__ void __launch_bounds__(FWD_THREADS, 1) norm_gate_kernel(const __grid_constant__ NormArgs a) {
     constexpr int TEAMS = FWD_THREADS / TPR, ES = U == 4 ? 4 : 2, P = U / 2;

@@ -29,10 +29,13 @@
 // The CTAs' column sums meet in the workspace and are added in order: no atomics,
 // equal calls give equal bits.
 //
-// Forward 109568 x 6144, fp32 residual: 1.37 ms, 5.9 TB/s; backward 36864 x 6144:
-// bf16 458 us (5.9 TB/s), layer norm 547, fp32 618 (6.6 TB/s).  What is left in
-// the bf16 layer norms, quantised ones above all (36864 x 6144: 350 us, 226 at
-// HBM's rate), is instructions: 53% of the issue slots, the rest latency.
+// Forward 109568 x 6144, fp32 residual: 1.39 ms, 5.8 TB/s; backward 36864 x 6144:
+// bf16 472 us alone (5.8 TB/s; 500 back to back), layer norm 542, fp32 layer norm
+// 630 (6.5 TB/s).  The layer norm into NVFP4 is furthest from HBM's rate (36864 x
+// 6144: 344 us of 226): 53% of the issue slots and the latency between reductions
+// and look-ups that two lanes (four with fp32 rows) make for one block.  Rows shared
+// by a cluster run at half (RMS) to a third (layer norm) of narrower rows' rate: 27648
+// x 8192 bf16 forward 677 and 885 us, backward 1080 and 1544.
 //
 // Shared by norm.cu (forward) and norm_bwd.cu: teams, units, the split of a row and
 // the launch.

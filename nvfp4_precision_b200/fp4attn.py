@@ -420,6 +420,9 @@ def fp4_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, softmax_sca
 
 # The calls below take a few microseconds on the device for one row.  Their
 # checks, outputs and library calls are made in native code (csrc/calls.cpp).
+# Errors found on the device (a non-finite input, a bad scale, a wait that ran
+# out) are in the status word of the workspace: a caller that wants to see them
+# passes one and reads it with fp4attn_read_status.
 
 def _load_calls():
     path = build.calls_path()
@@ -696,8 +699,11 @@ class FP4LinearSTE(torch.autograd.Function):
 def fp4_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Differentiable NVFP4 linear layer of bf16 x [..., K] with a bf16 or fp32
     weight [N, K] (fake quantisation of both under their computed scales, a
-    straight-through backward); K a multiple of 32.  The training-time
-    counterpart of fp4attn_linear, next to fp4_attention."""
+    straight-through backward); K a multiple of 32.  The weight's gradient is
+    rounded to bf16, then widened for an fp32 weight; a bias is rounded to bf16.
+    Forward and backward read the device status on the host and so wait for the
+    GPU.  The training-time counterpart of fp4attn_linear, next to
+    fp4_attention."""
     assert x.dtype is torch.bfloat16 and weight.dim() == 2 and x.shape[-1] == weight.shape[1], "x [..., K], weight [N, K]"
     return FP4LinearSTE.apply(x, weight, bias)
 
@@ -752,7 +758,9 @@ def norm_gate(x: torch.Tensor, h: Optional[torch.Tensor] = None, post_weight: Op
               layer_norm: bool = False, groups: Optional[int] = None):
     """Differentiable (y, z) of fp4attn_norm_gate for x [..., C] and h of x's
     shape; the rows are `groups` equal samples one after the other (as many as
-    gate, scale and shift [groups, C] have)."""
+    gate, scale and shift [groups, C] have).  The backward reads y, so that y is
+    not to be changed in place before it (autograd reports that).  Forward and
+    backward read the device status on the host and so wait for the GPU."""
     assert h is not None or (gate is None and post_weight is None), "gate and post_weight belong to a branch h"
     return NormGate.apply(x, h, post_weight, gate, pre_weight, scale, shift, eps, LAYER_NORM if layer_norm else 0, groups)
 
