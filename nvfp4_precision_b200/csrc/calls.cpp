@@ -2,8 +2,8 @@
 // new outputs and the C ABI call in one step.  A one-row norm runs in 4 us on the
 // device; marshalled in Python it took 15 us of host time, here under 7.
 //
-// The C ABI's addresses come from the binding (which chooses the library), as
-// does the exception that a status other than ok raises.  Wrong types, shapes
+// The C ABI's addresses come from the binding (which chooses the library), as do
+// the exceptions that a status other than ok and a lack of memory raise.  Wrong types, shapes
 // and layouts raise AssertionError, tensors off the current device ValueError.
 #include <Python.h>
 
@@ -34,6 +34,7 @@ struct Library {
     decltype(&fp4attn_norm_gate_backward) norm_gate_backward;
 } lib;
 PyObject* error_class = nullptr;
+PyObject* out_of_memory_class = nullptr;  // torch's, which an output without room raises
 
 void require(bool ok, const std::string& what) {
     if (!ok) throw Refused{PyExc_AssertionError, what};
@@ -368,6 +369,8 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
         PyErr_Clear();
         PyErr_SetString(e.type, e.what.c_str());
     } catch (const Failed&) {
+    } catch (const c10::OutOfMemoryError& e) {
+        PyErr_SetString(out_of_memory_class, e.what_without_backtrace());
     } catch (const std::exception& e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
     } catch (...) {
@@ -377,22 +380,25 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
 }
 
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
-    if (n != 8) {
-        PyErr_SetString(PyExc_TypeError, "an exception class and seven addresses expected");
+    if (n != 9) {
+        PyErr_SetString(PyExc_TypeError, "two exception classes and seven addresses expected");
         return nullptr;
     }
     void* p[7];
     for (int i = 0; i < 7; ++i) {
-        p[i] = PyLong_AsVoidPtr(args[1 + i]);
+        p[i] = PyLong_AsVoidPtr(args[2 + i]);
         if (PyErr_Occurred()) return nullptr;
     }
     lib = {reinterpret_cast<decltype(lib.quantize_rows)>(p[0]),   reinterpret_cast<decltype(lib.dequant_rows)>(p[1]),
            reinterpret_cast<decltype(lib.gemm)>(p[2]),            reinterpret_cast<decltype(lib.linear)>(p[3]),
            reinterpret_cast<decltype(lib.linear_backward)>(p[4]), reinterpret_cast<decltype(lib.norm_gate)>(p[5]),
            reinterpret_cast<decltype(lib.norm_gate_backward)>(p[6])};
+    Py_INCREF(args[0]);
+    Py_INCREF(args[1]);
     Py_XDECREF(error_class);
+    Py_XDECREF(out_of_memory_class);
     error_class = args[0];
-    Py_INCREF(error_class);
+    out_of_memory_class = args[1];
     Py_RETURN_NONE;
 }
 

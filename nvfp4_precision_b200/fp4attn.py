@@ -432,9 +432,10 @@ def _load_calls():
     loader = importlib.machinery.ExtensionFileLoader(name, path)
     module = importlib.util.module_from_spec(importlib.util.spec_from_file_location(name, path, loader=loader))
     loader.exec_module(module)
-    module.bind(Fp4AttnError, *(ctypes.cast(getattr(lib, "fp4attn_" + n), ctypes.c_void_p).value
-                                for n in ("quantize_rows", "dequant_rows", "gemm", "linear", "linear_backward", "norm_gate",
-                                          "norm_gate_backward")))
+    module.bind(Fp4AttnError, torch.OutOfMemoryError,
+                *(ctypes.cast(getattr(lib, "fp4attn_" + n), ctypes.c_void_p).value
+                  for n in ("quantize_rows", "dequant_rows", "gemm", "linear", "linear_backward", "norm_gate",
+                            "norm_gate_backward")))
     return module
 
 

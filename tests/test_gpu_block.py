@@ -574,3 +574,17 @@ def test_large_and_wide_calls_captured():
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(got, v))
     assert all(fa.fp4attn_read_status(t) == 0 for t in (ws, bws, *nws))
+
+
+def test_an_output_that_finds_no_memory():
+    """torch's own exception, and nothing launched: 2^22 x 2^22 results are 35 TB."""
+    fa = _fa()
+    rows = 1 << 22
+    codes = torch.zeros(rows, 16, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(fa.fp4attn_scale_tile_bytes(rows, 32), dtype=torch.uint8, device="cuda")
+    with pytest.raises(torch.OutOfMemoryError):
+        fa.fp4attn_gemm(codes, scales, codes, scales)
+    del codes, scales
+    torch.cuda.empty_cache()
+    x = torch.ones(2, 64, dtype=BF, device="cuda")
+    assert torch.isfinite(fa.fp4attn_norm_gate(x)["z"]).all()
