@@ -32,8 +32,8 @@
 // Forward 109568 x 6144, fp32 residual: 1.39 ms, 5.8 TB/s; backward 36864 x 6144:
 // bf16 472 us alone (5.8 TB/s; 500 back to back), layer norm 542, fp32 layer norm
 // 630 (6.5 TB/s).  The layer norm into NVFP4 is furthest from HBM's rate (36864 x
-// 6144: 344 us of 226): 53% of the issue slots and the latency between reductions
-// and look-ups that two lanes (four with fp32 rows) make for one block.  Rows shared
+// 6144: 344 us of 226): half of the issue slots, and the latency of reductions and
+// of look-ups that two lanes (four with fp32 rows) make for one block.  Rows shared
 // by a cluster run at half (RMS) to a third (layer norm) of narrower rows' rate: 27648
 // x 8192 bf16 forward 677 and 885 us, backward 1080 and 1544.
 //
